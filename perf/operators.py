@@ -312,7 +312,7 @@ def _run_own(s):
         abi.moe_gather_backward(s["rows"], s["slot_to_row"], s["x"], T, d, k, R, b["dx"], b["ws"])
         return b["dx"]
     if op == "gather_mxfp4":
-        abi.moe_gather_mxfp4(s["x"], T, d, k, s["row_slot"], s["seg"], E, R, b["codes"], b["scales"], b["ws"])
+        abi.moe_gather_mxfp4(s["x"], T, d, k, s["slot_to_row"], s["seg"], E, R, b["codes"], b["scales"], b["ws"])
         abi.moe_mxfp4_dequantize_rows(b["codes"], b["scales"], s["seg"], E, R, d, b["out"], b["ws"])
         return b["out"]
     act = abi.MOE_ACT_SWIGLU if case["act"] == "swiglu" else abi.MOE_ACT_GELU
