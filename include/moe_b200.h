@@ -111,6 +111,10 @@ typedef struct {
   const void* x_router;
   const float* logit_noise;
   float router_temperature;
+  /* MOE_LAYER_MXFP4 only (not read otherwise): scales of w1, w3 (SwiGLU) and w2 */
+  const void* w1_scales;
+  const void* w3_scales;
+  const void* w2_scales;
 } moe_layer_t;
 
 /* moe_layer_t.flags. MOE_LAYER_GATHER_IN_GEMM (bf16 only): moe_forward skips
@@ -143,6 +147,15 @@ typedef struct {
  * same as the default path's bit for bit. */
 #define MOE_LAYER_COMBINE_IN_GEMM 8
 
+/* MOE_LAYER_MXFP4 (bf16 layers; MOE_ERR_UNSUPPORTED otherwise): the experts'
+ * weights and the rows they read are in MXFP4 (see "MXFP4" below). w1, w3 and
+ * w2 point to codes and w1_scales, w3_scales and w2_scales to their scales, as
+ * moe_mxfp4_quantize_weights writes them; the gather quantises the rows and
+ * moe_expert_ffn_mxfp4 runs the experts. Router, x and out stay bf16. Not with
+ * MOE_LAYER_GATHER_IN_GEMM or MOE_LAYER_COMBINE_IN_GEMM
+ * (MOE_ERR_UNSUPPORTED). The views' x_perm and h are the codes. */
+#define MOE_LAYER_MXFP4 32
+
 /* Device pointers into a moe_forward workspace where that call leaves its
  * intermediate results (see moe_forward_views). */
 typedef struct {
@@ -158,8 +171,9 @@ typedef struct {
   int32_t* slot_to_row;  /* [T * k] */
   int32_t* row_slot;     /* [rows_max] */
   uint8_t* drop_mask;    /* [T * k] */
-  void* x_perm;          /* [rows_max, d]; NULL with MOE_LAYER_GATHER_IN_GEMM */
-  void* h;               /* [rows_max, F] */
+  void* x_perm;          /* [rows_max, d]; NULL with MOE_LAYER_GATHER_IN_GEMM;
+                            codes [rows_max, d / 2] with MOE_LAYER_MXFP4 */
+  void* h;               /* [rows_max, F]; codes [rows_max, F / 2] with MOE_LAYER_MXFP4 */
   void* y_perm;          /* [rows_max, d]; NULL with MOE_LAYER_COMBINE_IN_GEMM */
   int64_t rows_max;
   int64_t capacity;      /* C, or -1 when dropless */
@@ -471,6 +485,122 @@ MOE_API moe_status_t moe_expert_ffn(const void* x_perm, const void* w1, const vo
 MOE_API moe_status_t moe_combine(const void* y_perm, const float* topk_w, const int32_t* slot_to_row,
                          moe_dtype_t dtype, int T, int d, int k, int64_t rows_max, void* out,
                          void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* --------------------------------------------- gather and combine backward
+ * The gradients of the rows' way to the experts and back ("MegaBlocks",
+ * section 4.3: the gather reorders, the scatter weighs and sums; the pages
+ * print no backward, this is the chain rule of the two forwards above). With
+ * moe_route_backward they make the layer's backward around the experts' own:
+ * moe_combine_backward gives d_y_perm to the experts' backward and d_topk_w to
+ * moe_route_backward, and moe_gather_backward adds the experts' d_x_perm to
+ * the router's dx.
+ *
+ * Combine backward, out = sum_j w[t,j] y[row(t,j)]:
+ *   d_y_perm[row(t,j)] = topk_w[t,j] * d_out[t]   (fp32, rounded once to dtype)
+ *   d_topk_w[t,j]      = <d_out[t], y_perm[row(t,j)]> in fp32, 0 for a dropped slot
+ *   d_out [T, d] (dtype)      y_perm [rows_max, d] (dtype; may be NULL when
+ *   topk_w [T, k] fp32        d_topk_w is NULL)
+ *   slot_to_row [T * k]       from moe_permute or moe_permute_binned
+ *   d_y_perm  out [rows_max, d] (dtype) or NULL. Rows that hold no slot (past
+ *             seg_offsets[E], padding rows of the binned layout) are not written
+ *   d_topk_w  out [T, k] fp32 or NULL
+ * Two slots with the same row (no permute gives that) race on d_y_perm.
+ * A row index >= rows_max sets MOE_DEVERR_ROW_RANGE and counts as dropped.
+ *   ws  >= 256 bytes (control block)
+ * d: a multiple of 128 (bf16) or 4 (f32). No output may overlap an input.
+ * Deterministic (no atomics). */
+MOE_API moe_status_t moe_combine_backward(const void* d_out, const void* y_perm, const float* topk_w,
+                                          const int32_t* slot_to_row, moe_dtype_t dtype, int T,
+                                          int d, int k, int64_t rows_max, void* d_y_perm,
+                                          float* d_topk_w, void* ws, size_t ws_bytes,
+                                          moe_stream_t stream);
+
+/* Gather backward:
+ *   dx[t] = dx_in[t] + sum over the kept slots j of d_x_perm[slot_to_row[t,j]]
+ * in fp32 (dx_in first, then j ascending), rounded once to dtype; dx_in[t] (or
+ * zero) for a token whose every slot was dropped.
+ *   d_x_perm [rows_max, d] (dtype)   dx_in [T, d] (dtype) or NULL (nothing
+ *   added)   dx out [T, d] (dtype); dx may be dx_in itself.
+ * Limits, errors and ws as moe_combine_backward. Deterministic. */
+MOE_API moe_status_t moe_gather_backward(const void* d_x_perm, const int32_t* slot_to_row,
+                                         const void* dx_in, moe_dtype_t dtype, int T, int d, int k,
+                                         int64_t rows_max, void* dx, void* ws, size_t ws_bytes,
+                                         moe_stream_t stream);
+
+/* ------------------------------------------------------------------ MXFP4
+ * Experts in microscaled 4-bit floating point: OCP Microscaling Formats
+ * (version 1.0), MXFP4. Blocks of 32 values share one scale byte s (E8M0:
+ * 2^(s - 127), 255: NaN); each value is a 4-bit E2M1 code (sign bit, then
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6). Quantising a block with largest magnitude a:
+ *   s = max(floor(log2 a) - 2 + 127, 0)   (0 for a block of zeros)
+ *   code = value * 2^(127 - s) to the nearest E2M1 value, ties to the even
+ *   code, magnitudes above 6 to 6; the scaling is exact.
+ * A block that holds an Inf or a NaN gets s = 255 and reads back as NaN.
+ * Codes: two to a byte, the earlier value in the low half.
+ * Scales: tiles of 128 rows x 4 blocks (128 values), 512 bytes each; row r and
+ * block b of a tile at byte (r % 32) * 16 + (r / 32) * 4 + b; the d / 128 (or
+ * F / 128) tiles of one group of 128 rows in the order of the blocks. The
+ * row groups:
+ *   weights [E, K, N] (blocks along K; stored as codes [E, N, K / 2]): group
+ *     e * N / 128 + n / 128, row n % 128
+ *   rows sorted by expert (blocks along the row; codes [rows_max, K / 2]):
+ *     row r of expert e in group seg_offsets[e] / 128 + e + (r - seg_offsets[e])
+ *     / 128, row (r - seg_offsets[e]) % 128. Scales of rows that hold no slot
+ *     are not written and never used.
+ * Every K, N, d and F a multiple of 128 (MOE_ERR_UNSUPPORTED otherwise),
+ * 1 <= E <= 256; the dtype is that of the values (MOE_BF16 or MOE_F32). */
+
+/* Bytes of the scales of weights [E, K, N], and of rows [rows_max, K]. */
+MOE_API size_t moe_mxfp4_weight_scales_size(int E, int K, int N);
+MOE_API size_t moe_mxfp4_row_scales_size(int64_t rows_max, int E, int K);
+
+/* Expert weights w [E, K, N] (dtype) to codes [E, N, K / 2] and scales, once
+ * when the weights are loaded; and back (exact in bf16 and fp32, but for
+ * magnitudes below the dtype's subnormals). */
+MOE_API moe_status_t moe_mxfp4_quantize_weights(const void* w, moe_dtype_t dtype, int E, int K, int N,
+                                                void* codes, void* scales, moe_stream_t stream);
+MOE_API moe_status_t moe_mxfp4_dequantize_weights(const void* codes, const void* scales,
+                                                  moe_dtype_t dtype, int E, int K, int N, void* w,
+                                                  moe_stream_t stream);
+
+/* Gather and quantise in one pass: each token's row x[t] (dtype, d values) is
+ * read and quantised once and written to the row of each of its kept slots.
+ *   slot_to_row [T * k], seg_offsets [E + 1] from moe_permute or moe_permute_binned
+ *   codes  out [rows_max, d / 2]; rows that hold no slot are not written
+ *   scales out moe_mxfp4_row_scales_size(rows_max, E, d) bytes
+ *   ws     >= 256 bytes (control block). A row index at or past
+ *          min(seg_offsets[E], rows_max) sets MOE_DEVERR_ROW_RANGE and is skipped. */
+MOE_API moe_status_t moe_gather_mxfp4(const void* x, moe_dtype_t dtype, int T, int d, int k,
+                                      const int32_t* slot_to_row, const int32_t* seg_offsets, int E,
+                                      int64_t rows_max, void* codes, void* scales, void* ws,
+                                      size_t ws_bytes, moe_stream_t stream);
+
+/* Rows r < seg_offsets[E] read back as values: out [rows_max, K] (dtype); rows
+ * past them are not written. Padding rows of the binned layout read back as
+ * whatever their codes hold.   ws >= 256 bytes (control block) */
+MOE_API moe_status_t moe_mxfp4_dequantize_rows(const void* codes, const void* scales,
+                                               const int32_t* seg_offsets, int E, int64_t rows_max,
+                                               int K, moe_dtype_t dtype, void* out, void* ws,
+                                               size_t ws_bytes, moe_stream_t stream);
+
+/* moe_expert_ffn on MXFP4 rows and weights: both products multiply E2M1 codes
+ * with their block scales on the tensor cores and sum in fp32; the activation
+ * is fp32; h is quantised to MXFP4 along F (blocks of 32), y_perm is bf16.
+ *   x_codes [rows_max, d / 2], x_scales   as moe_gather_mxfp4 writes them
+ *   w1, w3 (SwiGLU; NULL for GELU) [E, F, d / 2], w2 [E, d, F / 2] and their
+ *     scales, as moe_mxfp4_quantize_weights writes them from [E, d, F] and [E, F, d]
+ *   h_codes [rows_max, F / 2], h_scales (moe_mxfp4_row_scales_size(rows_max,
+ *     E, F) bytes): out, the intermediate
+ *   y_perm  out [rows_max, d] bf16; rows past seg_offsets[E] are not written
+ *   ws      >= moe_expert_ffn_mxfp4_workspace_size(rows_max, d, F, E) bytes */
+MOE_API size_t moe_expert_ffn_mxfp4_workspace_size(int64_t rows_max, int d, int F, int E);
+MOE_API moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_scales, const void* w1,
+                                          const void* w1_scales, const void* w3, const void* w3_scales,
+                                          const void* w2, const void* w2_scales, moe_act_t act,
+                                          int64_t rows_max, int d, int F, int E,
+                                          const int32_t* seg_offsets, void* h_codes, void* h_scales,
+                                          void* y_perm, void* ws, size_t ws_bytes,
+                                          moe_stream_t stream);
 
 /* ---------------------------------------------------------------- forward
  * The whole layer on one stream with no host synchronisation: route ->

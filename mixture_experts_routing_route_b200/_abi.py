@@ -24,6 +24,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_INVALID", 3: "MOE_ERR_UNSU
 MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1
 MOE_LAYER_GATHER_IN_GEMM, MOE_LAYER_BINNED, MOE_LAYER_Z_LOSS, MOE_LAYER_COMBINE_IN_GEMM = 1, 2, 4, 8
+MOE_LAYER_MXFP4 = 32
 DEVERR_EXPERT_RANGE, DEVERR_ROW_RANGE, DEVERR_TIMEOUT = 1, 2, 4
 
 
@@ -97,6 +98,24 @@ _SIGS = {
                                c_size_t, c_void_p]),
     "moe_combine": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int64,
                             c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_combine_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                     c_int, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
+                                     c_void_p]),
+    "moe_gather_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                    c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_mxfp4_weight_scales_size": (c_size_t, [c_int, c_int, c_int]),
+    "moe_mxfp4_row_scales_size": (c_size_t, [c_int64, c_int, c_int]),
+    "moe_mxfp4_quantize_weights": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p,
+                                           c_void_p, c_void_p]),
+    "moe_mxfp4_dequantize_weights": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                             c_void_p, c_void_p]),
+    "moe_gather_mxfp4": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
+                                 c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_mxfp4_dequantize_rows": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int,
+                                          c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_expert_ffn_mxfp4_workspace_size": (c_size_t, [c_int64, c_int, c_int, c_int]),
+    "moe_expert_ffn_mxfp4": (c_int, [c_void_p] * 8 + [c_int, c_int64, c_int, c_int, c_int]
+                             + [c_void_p] * 5 + [c_size_t, c_void_p]),
     "moe_ep_send_plan": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p,
                                  c_size_t, c_void_p]),
     "moe_ep_recv_plan": (c_int, [c_void_p, c_int, c_int, c_int64, c_void_p, c_void_p, c_void_p,
@@ -280,6 +299,62 @@ def moe_combine(y_perm, topk_w, slot_to_row, T, d, k, rows_max, out, ws, stream=
     _check("moe_combine", _lib.moe_combine(
         _ptr(y_perm), _ptr(topk_w), _ptr(slot_to_row), dtype_code(out.dtype), T, d, k,
         int(rows_max), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_combine_backward(d_out, y_perm, topk_w, slot_to_row, T, d, k, rows_max, d_y_perm, d_topk_w,
+                         ws, stream=None):
+    _check("moe_combine_backward", _lib.moe_combine_backward(
+        _ptr(d_out), _ptr(y_perm), _ptr(topk_w), _ptr(slot_to_row), dtype_code(d_out.dtype), T, d,
+        k, int(rows_max), _ptr(d_y_perm), _ptr(d_topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_gather_backward(d_x_perm, slot_to_row, dx_in, T, d, k, rows_max, dx, ws, stream=None):
+    _check("moe_gather_backward", _lib.moe_gather_backward(
+        _ptr(d_x_perm), _ptr(slot_to_row), _ptr(dx_in), dtype_code(dx.dtype), T, d, k,
+        int(rows_max), _ptr(dx), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_mxfp4_weight_scales_size(E: int, K: int, N: int) -> int:
+    return _lib.moe_mxfp4_weight_scales_size(E, K, N)
+
+
+def moe_mxfp4_row_scales_size(rows_max: int, E: int, K: int) -> int:
+    return _lib.moe_mxfp4_row_scales_size(int(rows_max), E, K)
+
+
+def moe_mxfp4_quantize_weights(w, E, K, N, codes, scales, stream=None):
+    _check("moe_mxfp4_quantize_weights", _lib.moe_mxfp4_quantize_weights(
+        _ptr(w), dtype_code(w.dtype), E, K, N, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def moe_mxfp4_dequantize_weights(codes, scales, E, K, N, w, stream=None):
+    _check("moe_mxfp4_dequantize_weights", _lib.moe_mxfp4_dequantize_weights(
+        _ptr(codes), _ptr(scales), dtype_code(w.dtype), E, K, N, _ptr(w), _stream(stream)))
+
+
+def moe_gather_mxfp4(x, T, d, k, slot_to_row, seg_offsets, E, rows_max, codes, scales, ws,
+                     stream=None):
+    _check("moe_gather_mxfp4", _lib.moe_gather_mxfp4(
+        _ptr(x), dtype_code(x.dtype), T, d, k, _ptr(slot_to_row), _ptr(seg_offsets), E,
+        int(rows_max), _ptr(codes), _ptr(scales), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_mxfp4_dequantize_rows(codes, scales, seg_offsets, E, rows_max, K, out, ws, stream=None):
+    _check("moe_mxfp4_dequantize_rows", _lib.moe_mxfp4_dequantize_rows(
+        _ptr(codes), _ptr(scales), _ptr(seg_offsets), E, int(rows_max), K, dtype_code(out.dtype),
+        _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -> int:
+    return _lib.moe_expert_ffn_mxfp4_workspace_size(int(rows_max), d, F, E)
+
+
+def moe_expert_ffn_mxfp4(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales, act,
+                         rows_max, d, F, E, seg_offsets, h_codes, h_scales, y_perm, ws, stream=None):
+    _check("moe_expert_ffn_mxfp4", _lib.moe_expert_ffn_mxfp4(
+        _ptr(x_codes), _ptr(x_scales), _ptr(w1), _ptr(w1_scales), _ptr(w3), _ptr(w3_scales),
+        _ptr(w2), _ptr(w2_scales), act, int(rows_max), d, F, E, _ptr(seg_offsets), _ptr(h_codes),
+        _ptr(h_scales), _ptr(y_perm), _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def moe_ep_send_plan(kept_counts, seg_offsets, E, world, send_rows, send_offsets, ws, stream=None):

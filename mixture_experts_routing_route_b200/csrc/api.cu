@@ -520,6 +520,169 @@ moe_status_t moe_combine(const void* y_perm, const float* topk_w, const int32_t*
                                   static_cast<Control*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+moe_status_t moe_combine_backward(const void* d_out, const void* y_perm, const float* topk_w,
+                                  const int32_t* slot_to_row, moe_dtype_t dtype, int T, int d, int k,
+                                  int64_t rows_max, void* d_y_perm, float* d_topk_w, void* ws,
+                                  size_t ws_bytes, moe_stream_t stream) {
+  MOE_CHECK(check_dims(dtype, T, d, k, k));
+  if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_NEED(ws);
+  if (ws_bytes < sizeof(Control)) return MOE_ERR_WORKSPACE;
+  MOE_OPT(y_perm);
+  MOE_OPT(d_y_perm);
+  MOE_OPT(d_topk_w);
+  if (T > 0 && (d_y_perm != nullptr || d_topk_w != nullptr)) {
+    MOE_NEED(slot_to_row);
+    if (rows_max > 0) MOE_NEED(d_out);
+    if (d_y_perm != nullptr) MOE_NEED(topk_w);
+    if (d_topk_w != nullptr && rows_max > 0) MOE_NEED(y_perm);
+  }
+  return from_cuda(launch_combine_backward(d_out, y_perm, topk_w, slot_to_row, esize(dtype), T, d, k,
+                                           rows_max, d_y_perm, d_topk_w, static_cast<Control*>(ws),
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_gather_backward(const void* d_x_perm, const int32_t* slot_to_row, const void* dx_in,
+                                 moe_dtype_t dtype, int T, int d, int k, int64_t rows_max, void* dx,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_CHECK(check_dims(dtype, T, d, k, k));
+  if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_NEED(ws);
+  if (ws_bytes < sizeof(Control)) return MOE_ERR_WORKSPACE;
+  MOE_OPT(dx_in);
+  if (T > 0) {
+    MOE_NEED(slot_to_row);
+    MOE_NEED(dx);
+    if (rows_max > 0) MOE_NEED(d_x_perm);
+  }
+  return from_cuda(launch_gather_backward(d_x_perm, slot_to_row, dx_in, esize(dtype), T, d, k, rows_max,
+                                          dx, static_cast<Control*>(ws),
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static moe_status_t check_mxfp4(moe_dtype_t dtype, int E, int K, int N) {
+  if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_INVALID;
+  if (E < 1 || E > 256 || K <= 0 || N <= 0) return MOE_ERR_INVALID;
+  if (K % 128 != 0 || N % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_mxfp4_weight_scales_size(int E, int K, int N) {
+  if (E < 1 || K < 1 || N < 1) return 0;
+  return static_cast<size_t>(E) * ((static_cast<size_t>(N) + 127) / 128) * ((static_cast<size_t>(K) + 127) / 128) * 512;
+}
+
+size_t moe_mxfp4_row_scales_size(int64_t rows_max, int E, int K) {
+  if (rows_max < 0 || E < 1 || K < 1) return 0;
+  return (static_cast<size_t>(rows_max) / 128 + E) * ((static_cast<size_t>(K) + 127) / 128) * 512;
+}
+
+moe_status_t moe_mxfp4_quantize_weights(const void* w, moe_dtype_t dtype, int E, int K, int N, void* codes,
+                                        void* scales, moe_stream_t stream) {
+  MOE_CHECK(check_mxfp4(dtype, E, K, N));
+  if (K / 128 > 65535) return MOE_ERR_UNSUPPORTED;  // K tiles are the grid's y dimension
+  MOE_NEED(w);
+  MOE_NEED(codes);
+  MOE_NEED(scales);
+  return from_cuda(launch_mxfp4_quantize_weights(w, dtype, E, K, N, static_cast<uint8_t*>(codes),
+                                                 static_cast<uint8_t*>(scales),
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_mxfp4_dequantize_weights(const void* codes, const void* scales, moe_dtype_t dtype, int E,
+                                          int K, int N, void* w, moe_stream_t stream) {
+  MOE_CHECK(check_mxfp4(dtype, E, K, N));
+  if (K / 128 > 65535) return MOE_ERR_UNSUPPORTED;
+  MOE_NEED(codes);
+  MOE_NEED(scales);
+  MOE_NEED(w);
+  return from_cuda(launch_mxfp4_dequantize_weights(static_cast<const uint8_t*>(codes),
+                                                   static_cast<const uint8_t*>(scales), dtype, E, K, N, w,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_gather_mxfp4(const void* x, moe_dtype_t dtype, int T, int d, int k,
+                              const int32_t* slot_to_row, const int32_t* seg_offsets, int E,
+                              int64_t rows_max, void* codes, void* scales, void* ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+  MOE_CHECK(check_dims(dtype, T, d, E, k));
+  if (d % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_NEED(ws);
+  if (ws_bytes < sizeof(Control)) return MOE_ERR_WORKSPACE;
+  if (T > 0 && rows_max > 0) {
+    MOE_NEED(x);
+    MOE_NEED(slot_to_row);
+    MOE_NEED(seg_offsets);
+    MOE_NEED(codes);
+    MOE_NEED(scales);
+  }
+  return from_cuda(launch_gather_mxfp4(x, dtype, T, d, k, slot_to_row, seg_offsets, E, rows_max,
+                                       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                                       static_cast<Control*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_mxfp4_dequantize_rows(const void* codes, const void* scales, const int32_t* seg_offsets,
+                                       int E, int64_t rows_max, int K, moe_dtype_t dtype, void* out, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream) {
+  MOE_CHECK(check_mxfp4(dtype, E, K, 128));
+  if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_NEED(ws);
+  if (ws_bytes < sizeof(Control)) return MOE_ERR_WORKSPACE;
+  if (rows_max > 0) {
+    MOE_NEED(codes);
+    MOE_NEED(scales);
+    MOE_NEED(seg_offsets);
+    MOE_NEED(out);
+  }
+  return from_cuda(launch_mxfp4_dequantize_rows(static_cast<const uint8_t*>(codes),
+                                                static_cast<const uint8_t*>(scales), seg_offsets, E, rows_max,
+                                                K, dtype, out, static_cast<Control*>(ws),
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_expert_ffn_mxfp4_workspace_size(int64_t rows_max, int d, int F, int E) {
+  if (rows_max < 0 || d < 1 || F < 1 || E < 1) return 0;
+  return align_up(sizeof(Control));
+}
+
+moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_scales, const void* w1,
+                                  const void* w1_scales, const void* w3, const void* w3_scales, const void* w2,
+                                  const void* w2_scales, moe_act_t act, int64_t rows_max, int d, int F, int E,
+                                  const int32_t* seg_offsets, void* h_codes, void* h_scales, void* y_perm,
+                                  void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_CHECK(check_mxfp4(MOE_BF16, E, d, F));
+  if (act != MOE_ACT_GELU && act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID;
+  if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_NEED(w1);
+  MOE_NEED(w1_scales);
+  MOE_NEED(w2);
+  MOE_NEED(w2_scales);
+  if (act == MOE_ACT_SWIGLU) {
+    MOE_NEED(w3);
+    MOE_NEED(w3_scales);
+  }
+  MOE_NEED(seg_offsets);
+  MOE_NEED(ws);
+  if (ws_bytes < moe_expert_ffn_mxfp4_workspace_size(rows_max, d, F, E)) return MOE_ERR_WORKSPACE;
+  if (rows_max > 0) {
+    MOE_NEED(x_codes);
+    MOE_NEED(x_scales);
+    MOE_NEED(h_codes);
+    MOE_NEED(h_scales);
+    MOE_NEED(y_perm);
+  }
+  // x is only read; the row type is shared with h, which is written
+  const MxRows x{static_cast<uint8_t*>(const_cast<void*>(x_codes)), static_cast<uint8_t*>(const_cast<void*>(x_scales))};
+  const MxRows h{static_cast<uint8_t*>(h_codes), static_cast<uint8_t*>(h_scales)};
+  auto weights = [](const void* c, const void* s) {
+    return MxWeights{static_cast<const uint8_t*>(c), static_cast<const uint8_t*>(s)};
+  };
+  return from_cuda(launch_ffn_mxfp4(x, weights(w1, w1_scales), weights(w3, w3_scales), weights(w2, w2_scales),
+                                    act, rows_max, d, F, E, seg_offsets, nullptr, h, y_perm,
+                                    static_cast<Control*>(ws), reinterpret_cast<cudaStream_t>(stream), nullptr));
+}
+
 moe_status_t moe_ep_send_plan(const int32_t* kept_counts, const int32_t* seg_offsets, int E,
                               int world, int32_t* send_rows, int32_t* send_offsets, void* ws,
                               size_t ws_bytes, moe_stream_t stream) {

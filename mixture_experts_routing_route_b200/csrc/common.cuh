@@ -345,6 +345,42 @@ cudaError_t launch_combine(const void* y, const float* w, const int32_t* slot_to
                            int T, int d, int k, int64_t rows_max, void* out, Control* ctl,
                            cudaStream_t s);
 
+// Backward of the combine (dy [rows_max, d] and dw [T, k], either may be NULL)
+// and of the gather (dx_in NULL: nothing added); see dispatch_backward.cu.
+cudaError_t launch_combine_backward(const void* dout, const void* y, const float* w,
+                                    const int32_t* slot_to_row, size_t elem, int T, int d, int k,
+                                    int64_t rows_max, void* dy, float* dw, Control* ctl,
+                                    cudaStream_t s);
+cudaError_t launch_gather_backward(const void* dx_perm, const int32_t* slot_to_row,
+                                   const void* dx_in, size_t elem, int T, int d, int k,
+                                   int64_t rows_max, void* dx, Control* ctl, cudaStream_t s);
+
+// MXFP4 (see mxfp4.cuh). Rows sorted by expert and expert weights [E, N, K].
+struct MxRows {
+  uint8_t* codes;   // [rows_max, K / 2]
+  uint8_t* scales;  // [rows_max / 128 + E] groups of K / 128 tiles
+};
+struct MxWeights {
+  const uint8_t* codes;   // [E, N, K / 2]
+  const uint8_t* scales;  // [E, N / 128, K / 128] tiles
+};
+cudaError_t launch_mxfp4_quantize_weights(const void* w, moe_dtype_t dt, int E, int K, int N,
+                                          uint8_t* codes, uint8_t* scales, cudaStream_t s);
+cudaError_t launch_mxfp4_dequantize_weights(const uint8_t* codes, const uint8_t* scales, moe_dtype_t dt,
+                                            int E, int K, int N, void* w, cudaStream_t s);
+cudaError_t launch_gather_mxfp4(const void* x, moe_dtype_t dt, int T, int d, int k,
+                                const int32_t* slot_to_row, const int32_t* seg, int E, int64_t rows_max,
+                                uint8_t* codes, uint8_t* scales, Control* ctl, cudaStream_t s);
+cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* seg,
+                                         int E, int64_t rows_max, int K, moe_dtype_t dt, void* out,
+                                         Control* ctl, cudaStream_t s);
+// The experts' FFN on MXFP4 rows and weights; y bf16. kept: rows of each
+// expert (binned layout), NULL: seg[e + 1] - seg[e].
+cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
+                             moe_act_t act, int64_t rows_max, int d, int F, int E, const int32_t* seg,
+                             const int32_t* kept, const MxRows& h, void* y, Control* ctl, cudaStream_t s,
+                             cudaEvent_t after_up);
+
 // Expert-parallel dispatch plans (ep.cu). Experts are owned in contiguous
 // blocks of e_loc per rank.
 cudaError_t launch_ep_send_plan(const int32_t* kept, const int32_t* seg, int world, int e_loc,

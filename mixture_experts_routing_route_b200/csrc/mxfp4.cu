@@ -1,0 +1,355 @@
+// Quantising to MXFP4 and reading back: expert weights, and token rows on
+// their way to the experts (see mxfp4.cuh for the format and the layout of
+// the scales).
+//
+// Weights [E, K, N] are stored along N but their blocks run along K, the
+// dimension the products sum over, and the tensor cores want K contiguous:
+// quantising transposes. Both directions stream the matrix once through
+// registers, a 128 x 128 tile per block of threads, and are bound by DRAM.
+#include "mxfp4.cuh"
+#include <algorithm>
+#include <type_traits>
+
+namespace moe {
+
+namespace {
+
+template <typename T> struct Pair;  // two neighbouring columns
+template <> struct Pair<__nv_bfloat16> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ float2 f32(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t raw(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+template <> struct Pair<float> {
+  using Raw = float2;
+  static __device__ __forceinline__ float2 f32(float2 v) { return v; }
+  static __device__ __forceinline__ float2 raw(float a, float b) { return make_float2(a, b); }
+};
+
+constexpr int kWTile = 128;     // tile of K and of N
+constexpr int kWThreads = 256;  // 64 column pairs x 4 blocks of 32 along K
+
+// One 128 (K) x 128 (N) tile: a thread holds 32 k of two neighbouring columns,
+// exactly one block of each, so that amax and codes need no other thread; a
+// warp's loads are 64 columns of one k row. Codes and scales go through shared
+// memory to leave as 64-byte row pieces and one 512-byte tile.
+template <typename T>
+__global__ void __launch_bounds__(kWThreads)
+quantize_weights(const T* __restrict__ w, int K, int N, uint8_t* __restrict__ codes,
+                 uint8_t* __restrict__ scales) {
+  pdl_begin();
+  __shared__ uint4 code_s[kWTile][5];  // 64 bytes a column, one vector of padding
+  __shared__ __align__(16) uint8_t scale_s[kScaleTile];
+  const int c = threadIdx.x & 63, kb = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * kWTile, k0 = blockIdx.y * kWTile;
+  const long long e = blockIdx.z;
+  const T* src = w + (static_cast<size_t>(e) * K + k0 + kb * 32) * N + n0 + 2 * c;
+  typename Pair<T>::Raw raw[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    raw[i] = __ldg(reinterpret_cast<const typename Pair<T>::Raw*>(src + static_cast<size_t>(i) * N));
+  uint32_t top[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float2 v = Pair<T>::f32(raw[i]);
+    top[0] = max(top[0], __float_as_uint(v.x) & 0x7fffffffu);
+    top[1] = max(top[1], __float_as_uint(v.y) & 0x7fffffffu);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = 2 * c + h;
+    const uint32_t sb = mx_scale_byte(top[h]);
+    const float inv = mx_inv_scale(sb);
+    uint32_t q[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 p = Pair<T>::f32(raw[8 * g + i]);
+        v[i] = (h == 0 ? p.x : p.y) * inv;
+      }
+      q[g] = sb == 255u ? 0u : e2m1x8(v);
+    }
+    code_s[n][kb] = make_uint4(q[0], q[1], q[2], q[3]);
+    scale_s[(n & 31) * 16 + (n >> 5) * 4 + kb] = static_cast<uint8_t>(sb);
+  }
+  __syncthreads();
+  uint8_t* dst = codes + (static_cast<size_t>(e) * N + n0) * (K / 2) + k0 / 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = threadIdx.x + i * kWThreads;  // 128 columns x 4 vectors
+    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(u >> 2) * (K / 2) + (u & 3) * 16) = code_s[u >> 2][u & 3];
+  }
+  if (threadIdx.x < kScaleTile / 16) {
+    const long long group = e * (N / 128) + blockIdx.x;
+    *reinterpret_cast<uint4*>(scales + mx_scale_at(group, K / 128, 0, 4 * blockIdx.y) + threadIdx.x * 16) =
+        *reinterpret_cast<const uint4*>(scale_s + threadIdx.x * 16);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWThreads)
+dequantize_weights(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int K, int N,
+                   T* __restrict__ w) {
+  pdl_begin();
+  __shared__ uint4 code_s[kWTile][5];
+  __shared__ uint4 scale_s[kScaleTile / 16];
+  const int c = threadIdx.x & 63, kb = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * kWTile, k0 = blockIdx.y * kWTile;
+  const long long e = blockIdx.z;
+  const uint8_t* src = codes + (static_cast<size_t>(e) * N + n0) * (K / 2) + k0 / 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = threadIdx.x + i * kWThreads;
+    code_s[u >> 2][u & 3] =
+        __ldg(reinterpret_cast<const uint4*>(src + static_cast<size_t>(u >> 2) * (K / 2) + (u & 3) * 16));
+  }
+  if (threadIdx.x < kScaleTile / 16) {
+    const long long group = e * (N / 128) + blockIdx.x;
+    scale_s[threadIdx.x] = __ldg(reinterpret_cast<const uint4*>(
+        scales + mx_scale_at(group, K / 128, 0, 4 * blockIdx.y) + threadIdx.x * 16));
+  }
+  __syncthreads();
+  float f[2];
+  uint32_t q[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = 2 * c + h;
+    f[h] = mx_scale(reinterpret_cast<const uint8_t*>(scale_s)[(n & 31) * 16 + (n >> 5) * 4 + kb]);
+    const uint4 v = code_s[n][kb];
+    q[h][0] = v.x; q[h][1] = v.y; q[h][2] = v.z; q[h][3] = v.w;
+  }
+  T* dst = w + (static_cast<size_t>(e) * K + k0 + kb * 32) * N + n0 + 2 * c;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float a = e2m1_value((q[0][i >> 3] >> (4 * (i & 7))) & 15u) * f[0];
+    const float b = e2m1_value((q[1][i >> 3] >> (4 * (i & 7))) & 15u) * f[1];
+    *reinterpret_cast<typename Pair<T>::Raw*>(dst + static_cast<size_t>(i) * N) = Pair<T>::raw(a, b);
+  }
+}
+
+// Eight consecutive values of a row.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(x[i] << 16);
+    v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(Pair<__nv_bfloat16>::raw(v[0], v[1]), Pair<__nv_bfloat16>::raw(v[2], v[3]),
+                                            Pair<__nv_bfloat16>::raw(v[4], v[5]), Pair<__nv_bfloat16>::raw(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+constexpr int kRowWarps = 8;
+constexpr int kRowIter = 4;                  // a unit: 4 x 256 values of one row
+constexpr int kRowChunk = kRowIter * 256;
+constexpr int kRowMaxE = 256;
+
+// Expert of row r: the last e with seg[e] <= r (empty experts share a start
+// with the one that has the row). Valid for seg[0] <= r < seg[E].
+__device__ __forceinline__ int row_expert(const int* seg, int E, int r) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (seg[mid] <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The rows on their way to the experts: a warp takes 1024 values of one token,
+// quantises them once and writes them to each of the token's rows. Four lanes
+// hold a block (8 values a lane), so a block's largest magnitude is two
+// shuffles away, and a lane's codes are one 4-byte store of a 128-byte run.
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32)
+gather_mxfp4(const T* __restrict__ x, int T_, int d, int k, const int32_t* __restrict__ slot_to_row,
+             const int32_t* __restrict__ seg, int E, long long rows_max, uint8_t* __restrict__ codes,
+             uint8_t* __restrict__ scales, Control* ctl) {
+  pdl_begin();
+  __shared__ int seg_s[kRowMaxE + 1];
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) seg_s[i] = __ldg(seg + i);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const long long R = min(static_cast<long long>(seg_s[E]), rows_max);
+  const int chunks = (d + kRowChunk - 1) / kRowChunk;
+  const long long units = static_cast<long long>(T_) * chunks;
+  const long long step = static_cast<long long>(gridDim.x) * kRowWarps;
+  for (long long u = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const long long t = u / chunks;
+    const int c0 = static_cast<int>(u - t * chunks) * kRowChunk;
+    float v[kRowIter][8];
+#pragma unroll
+    for (int i = 0; i < kRowIter; ++i) {
+      const int col = c0 + i * 256 + lane * 8;
+      if (col < d) {
+        load8(x + static_cast<size_t>(t) * d + col, v[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      }
+    }
+    uint32_t q[kRowIter], sw[kRowIter];  // codes; scale bytes of the lane's four neighbouring blocks
+#pragma unroll
+    for (int i = 0; i < kRowIter; ++i) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t sb = mx_scale_byte(top);
+      const float inv = mx_inv_scale(sb);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+      q[i] = sb == 255u ? 0u : e2m1x8(v[i]);
+      sw[i] = sb << (8 * ((lane >> 2) & 3));
+      sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
+      sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
+    }
+    for (int j = 0; j < k; ++j) {
+      const int row = __ldg(slot_to_row + t * k + j);
+      if (row < 0) continue;
+      if (row >= R) {
+        if (lane == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
+        continue;
+      }
+      const int e = row_expert(seg_s, E, row);
+      const int rank = row - seg_s[e];
+      if (rank < 0 || seg_s[e] < 0) {  // seg is not an ascending list from 0
+        if (lane == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
+        continue;
+      }
+      const long long group = seg_s[e] / 128 + e + rank / 128;
+#pragma unroll
+      for (int i = 0; i < kRowIter; ++i) {
+        const int col = c0 + i * 256 + lane * 8;
+        if (col >= d) continue;
+        *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(row) * (d / 2) + col / 2) = q[i];
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(scales + mx_scale_at(group, d / 128, rank & 127, col / 32)) = sw[i];
+      }
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32)
+dequantize_rows(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                const int32_t* __restrict__ seg, int E, long long rows_max, int K, T* __restrict__ out,
+                Control* ctl) {
+  pdl_begin();
+  __shared__ int seg_s[kRowMaxE + 1];
+  for (int i = threadIdx.x; i <= E; i += blockDim.x) seg_s[i] = __ldg(seg + i);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  long long R = seg_s[E];
+  if (R > rows_max || R < 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
+    R = R < 0 ? 0 : rows_max;
+  }
+  const int chunks = (K + kRowChunk - 1) / kRowChunk;
+  const long long units = R * chunks;
+  const long long step = static_cast<long long>(gridDim.x) * kRowWarps;
+  for (long long u = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const int row = static_cast<int>(u / chunks);
+    const int c0 = static_cast<int>(u - static_cast<long long>(row) * chunks) * kRowChunk;
+    const int e = row_expert(seg_s, E, row);
+    const int rank = row - seg_s[e];
+    if (rank < 0 || seg_s[e] < 0) {
+      if (lane == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
+      continue;
+    }
+    const long long group = seg_s[e] / 128 + e + rank / 128;
+    uint32_t q[kRowIter], sb[kRowIter];
+#pragma unroll
+    for (int i = 0; i < kRowIter; ++i) {
+      const int col = c0 + i * 256 + lane * 8;
+      q[i] = sb[i] = 0;
+      if (col < K) {
+        q[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(row) * (K / 2) + col / 2));
+        sb[i] = __ldg(scales + mx_scale_at(group, K / 128, rank & 127, col / 32));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowIter; ++i) {
+      const int col = c0 + i * 256 + lane * 8;
+      if (col >= K) continue;
+      const float f = mx_scale(sb[i]);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = e2m1_value((q[i] >> (4 * j)) & 15u) * f;
+      store8(out + static_cast<size_t>(row) * K + col, v);
+    }
+  }
+}
+
+int row_grid(long long units) {
+  return static_cast<int>(std::max<long long>(1, std::min<long long>((units + kRowWarps - 1) / kRowWarps, 8LL * num_sms())));
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp4_quantize_weights(const void* w, moe_dtype_t dt, int E, int K, int N,
+                                          uint8_t* codes, uint8_t* scales, cudaStream_t s) {
+  const dim3 grid(N / kWTile, K / kWTile, E);
+  if (dt == MOE_BF16)
+    return launch_pdl(quantize_weights<__nv_bfloat16>, grid, dim3(kWThreads), 0, s, false,
+                      static_cast<const __nv_bfloat16*>(w), K, N, codes, scales);
+  return launch_pdl(quantize_weights<float>, grid, dim3(kWThreads), 0, s, false,
+                    static_cast<const float*>(w), K, N, codes, scales);
+}
+
+cudaError_t launch_mxfp4_dequantize_weights(const uint8_t* codes, const uint8_t* scales, moe_dtype_t dt,
+                                            int E, int K, int N, void* w, cudaStream_t s) {
+  const dim3 grid(N / kWTile, K / kWTile, E);
+  if (dt == MOE_BF16)
+    return launch_pdl(dequantize_weights<__nv_bfloat16>, grid, dim3(kWThreads), 0, s, false, codes, scales,
+                      K, N, static_cast<__nv_bfloat16*>(w));
+  return launch_pdl(dequantize_weights<float>, grid, dim3(kWThreads), 0, s, false, codes, scales, K, N,
+                    static_cast<float*>(w));
+}
+
+cudaError_t launch_gather_mxfp4(const void* x, moe_dtype_t dt, int T, int d, int k,
+                                const int32_t* slot_to_row, const int32_t* seg, int E, int64_t rows_max,
+                                uint8_t* codes, uint8_t* scales, Control* ctl, cudaStream_t s) {
+  if (T <= 0 || rows_max <= 0) return cudaSuccess;
+  const int grid = row_grid(static_cast<long long>(T) * ((d + kRowChunk - 1) / kRowChunk));
+  if (dt == MOE_BF16)
+    return launch_pdl(gather_mxfp4<__nv_bfloat16>, dim3(grid), dim3(kRowWarps * 32), 0, s, false,
+                      static_cast<const __nv_bfloat16*>(x), T, d, k, slot_to_row, seg, E, rows_max, codes,
+                      scales, ctl);
+  return launch_pdl(gather_mxfp4<float>, dim3(grid), dim3(kRowWarps * 32), 0, s, false,
+                    static_cast<const float*>(x), T, d, k, slot_to_row, seg, E, rows_max, codes, scales, ctl);
+}
+
+cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* scales, const int32_t* seg,
+                                         int E, int64_t rows_max, int K, moe_dtype_t dt, void* out,
+                                         Control* ctl, cudaStream_t s) {
+  if (rows_max <= 0) return cudaSuccess;
+  const int grid = row_grid(rows_max * ((K + kRowChunk - 1) / kRowChunk));
+  if (dt == MOE_BF16)
+    return launch_pdl(dequantize_rows<__nv_bfloat16>, dim3(grid), dim3(kRowWarps * 32), 0, s, false, codes,
+                      scales, seg, E, rows_max, K, static_cast<__nv_bfloat16*>(out), ctl);
+  return launch_pdl(dequantize_rows<float>, dim3(grid), dim3(kRowWarps * 32), 0, s, false, codes, scales, seg,
+                    E, rows_max, K, static_cast<float*>(out), ctl);
+}
+
+}  // namespace moe
