@@ -9,20 +9,33 @@
 //      scales of h); or the plain bf16 store of the down projection. Sums and
 //      activations are fp32; h is rounded once (to E2M1), y once (to bf16).
 //
-// CTA = 6 warps, one CTA per SM, persistent over tiles:
-//   warp 0   producer: per stage (256 values of K) the 128-row A box and the B
-//            boxes by TMA (128 bytes = 256 codes a row, 128-byte swizzle), and
-//            the scales of both by bulk copies (1 KB per 128 rows)
-//   warp 1   MMA issuer: per 128 values of K one thread copies the scale tiles
-//            to tensor memory (tcgen05.cp, replicated to the four lane
-//            quarters) and issues two MMAs of K = 64 with them
-//   warps 2-5 epilogue: a thread per row, 32 columns (one block) at a time
+// The two CTAs of a cluster compute one 256-row x N tile together
+// (cta_group::2), persistently. CTA r holds A rows [row0 + 128 r, +128) and its
+// half of the B columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output
+// columns), its rows' scales and the scales of all B columns. Ten warps a CTA:
+//   warp 0   producer: per stage (256 values of K) the A and B boxes by TMA (128
+//            bytes = 256 codes a row, 128-byte swizzle) and the scale tiles (two
+//            of 512 bytes per 128 rows)
+//   warp 1   MMA issuer (even CTA): per 128 values of K one thread copies the
+//            scale tiles to tensor memory of both CTAs (tcgen05.cp, replicated
+//            to the four lane quarters) and issues two MMAs of K = 64
+//   warps 2-9 epilogue: a thread per row and half of the columns, 32 columns
+//            (one block) at a time; two warps per scheduler hide the latency of
+//            the activation's exponentials
+// Why pairs: an SM takes about 52 bytes per clock from L2 (measured), and a
+// 128 x 256 tile of one CTA needs 48 KB of operands per 512 clocks of MMA, 94
+// bytes per clock; a pair's CTA needs 35 KB.
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit in
 // 512 columns, so the accumulators overlap by 32 columns (columns 0-255 and
 // 224-479) and the scales use 480-511 (two sets of 12, taken in turn). The
 // epilogue reads the overlapping columns first and frees them at once; the
 // next tile's MMAs start then, while the rest of the tile is still read.
+//
+// Work is handed out dynamically, as in the bf16 CTA-pair kernel: the even
+// CTA's producer takes the next tile from a counter in the control block and
+// publishes it to the pair's other roles, so that pairs sharing a weight block
+// read it at nearly the same time.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
 #include "gemm_common.cuh"
 #include "mxfp4.cuh"
@@ -35,20 +48,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 namespace {
 
-constexpr int kTileM = 128;
+constexpr int kTileM = 256;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (256 values of K)
-constexpr int kThreads = 192;
-constexpr int kStages = 4;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;               // per CTA
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kUnitSlots = 4;              // ring of tiles published to the pair's roles
+constexpr uint32_t kUnitReaders = 2 + 2 * kEpiWarps;  // peer producer, MMA thread, epilogue warps
 
 enum { EPI_SWIGLU = 0, EPI_GELU = 1, EPI_STORE = 2 };
 
 struct MxArgs {
   const int32_t* seg;    // [E+1] row segment offsets
   const int32_t* kept;   // [E] rows of each expert from seg[e] (binned layout), or null
-  const uint8_t* sa;     // scales of A
-  const uint8_t* sb0;    // scales of B (W_gate / W1 / W2)
-  const uint8_t* sb1;    // scales of W_up (SwiGLU)
   uint8_t* out_codes;    // up projection: h codes [rows_max, N/2]
   uint8_t* out_scales;   // up projection: h scales
   __nv_bfloat16* out;    // down projection: [rows_max, N]
@@ -68,35 +79,53 @@ __host__ __device__ constexpr uint32_t make_idesc_mxf4(int M, int N, uint32_t sf
          (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 29);
 }
 
+// True in one thread of a converged warp, the same one every time. The tensor
+// core's and TMA's instructions take warp-uniform operands: issued under this
+// predicate from code that the whole warp runs they cost a few cycles each,
+// from a branch that one lane took (lane == 0) about 80 (measured: a stage's
+// eleven took 885 cycles, more than the MMAs themselves).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
       : "memory");
 }
 
-// One 512-byte scale tile (32 rows of 16 bytes, 8-row groups 128 bytes apart)
-// to 4 columns of tensor memory, replicated to the four 32-lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t smem_addr) {
-  const uint64_t desc = static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                        (static_cast<uint64_t>(1u) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// Descriptor of scale tiles at a shared-memory address: no swizzle, 32 rows of
+// 16 bytes, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t make_scale_desc(uint32_t smem_addr) {
+  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
+         (static_cast<uint64_t>(1u) << 46);
+}
+
+// One 512-byte scale tile of each CTA of the pair to 4 columns of its tensor memory, replicated to the
+// four 32-lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
 template <int EPI, int NMMA>
 struct Cfg {
-  static constexpr int NB = NMMA / 128;  // 128-column B boxes
+  static constexpr int NB = NMMA / 128;                  // scale tiles of B per 128 values of K
   static constexpr int OUT_N = EPI == EPI_SWIGLU ? NMMA / 2 : NMMA;
-  static constexpr int OPERANDS = (1 + NB) * kBoxBytes;
+  static constexpr int B_ROWS = NMMA / 2;                // B columns this CTA loads
+  static constexpr int OPERANDS = kBoxBytes + B_ROWS * 128;
   static constexpr int SCALES = (1 + NB) * 2 * kScaleTile;
   static constexpr int STAGE_BYTES = OPERANDS + SCALES;  // a multiple of 1024
+  static constexpr int STAGES = NMMA == 256 ? 6 : 8;
   static constexpr int ACC1 = NMMA == 256 ? 224 : 128;   // first column of the second accumulator
   static constexpr int SF_COL = 480;
   static constexpr int TMEM_COLS = 512;
-  static constexpr size_t SMEM = static_cast<size_t>(kStages) * STAGE_BYTES + 1024;
+  static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + 1024;
 };
 
 struct MxTile {
@@ -142,20 +171,19 @@ __device__ __forceinline__ uint32_t quantise_block(float (&h)[32], uint4& codes)
   return sb;
 }
 
-// One warp's 32 rows of a tile. first: the 32-column group to read first (it
-// holds the columns that overlap the other accumulator); `free_overlap` is
-// called once its loads are done.
-template <int EPI, int OUT_N, typename Free>
-__device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, const MxTile& t, int wrow, int lane,
-                                         int first, Free&& free_overlap) {
-  constexpr int G = OUT_N / 32;
-  const int r = wrow + lane;  // row in the tile
-  const bool valid = r < t.rows;
-  const size_t row = static_cast<size_t>(t.row0) + r;
-  uint32_t sw[G / 4] = {};
+// One warp's 32 rows (crow: the first in the tile) and the column groups [g0,
+// g0 + G) of 32. reverse: the last group first; `free_overlap` is called once
+// the first group's loads are done.
+template <int EPI, int OUT_N, int G, typename Free>
+__device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, const MxTile& t, int crow, int lane,
+                                         int g0, bool reverse, Free&& free_overlap) {
+  const bool valid = crow + lane < t.rows;
+  const size_t row = static_cast<size_t>(t.row0) + crow + lane;
+  uint32_t sw = 0;
 #pragma unroll 1
   for (int gi = 0; gi < G; ++gi) {
-    const int g = first == 0 ? gi : (gi == 0 ? G - 1 : gi - 1);
+    const int gl = reverse ? G - 1 - gi : gi;
+    const int g = g0 + gl;
     float h[32];
     uint32_t v[32];
     if constexpr (EPI == EPI_SWIGLU) {
@@ -187,18 +215,18 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
       uint4 codes;
       const uint32_t sb = quantise_block(h, codes);
       if (valid) *reinterpret_cast<uint4*>(args.out_codes + row * (args.N / 2) + col / 2) = codes;
-#pragma unroll
-      for (int w = 0; w < G / 4; ++w)
-        if (w == (g >> 2)) sw[w] |= sb << (8 * (g & 3));
+      sw |= sb << (8 * gl);
     }
   }
   if constexpr (EPI != EPI_STORE) {
     if (valid) {
-      const long long group = t.row0 - t.mt * kTileM;  // seg[e]
-#pragma unroll
-      for (int w = 0; w < G / 4; ++w)
-        *reinterpret_cast<uint32_t*>(args.out_scales + mx_scale_at(group / 128 + t.e + t.mt, args.N / 128, r,
-                                                                   t.n0 / 32 + 4 * w)) = sw[w];
+      // this warp's rows lie in one group of 128 of the expert's rows
+      const int r = t.mt * kTileM + crow + lane;
+      const long long group = (t.row0 - t.mt * kTileM) / 128 + t.e + r / 128;
+      uint8_t* dst = args.out_scales + mx_scale_at(group, args.N / 128, r & 127, t.n0 / 32 + g0);
+      static_assert(G == 2 || G == 4, "half of 128 or of 256 columns");
+      if constexpr (G == 4) *reinterpret_cast<uint32_t*>(dst) = sw;
+      else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sw);
     }
   }
 }
@@ -206,12 +234,16 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
 template <int EPI, int NMMA>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                  const __grid_constant__ CUtensorMap tmB1, MxArgs args) {
+                  const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmSA,
+                  const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1, MxArgs args) {
   pdl_begin();
   using C = Cfg<EPI, NMMA>;
+  constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2], tfree_bar[2], drain_bar;
+  __shared__ __align__(8) uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
+  __shared__ volatile int unit_ring[kUnitSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int seg_s[kMaxE + 1];
   __shared__ int cnt_s[kMaxE];
@@ -220,6 +252,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int E = args.E;
+  const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the MMAs
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
 
@@ -232,165 +265,275 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __syncthreads();
   if (warp == 0) build_schedule<kTileM>(args, args.N / C::OUT_N, seg_s, cnt_s, tile_start_s, lane);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], kEpiWarps); }
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * kEpiWarps); }
+    for (int i = 0; i < kUnitSlots; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_empty[i], kUnitReaders);
+    }
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(&tmem_base_s, C::TMEM_COLS);
-    tmem_relinquish();
+    tmem_alloc_pair(&tmem_base_s, C::TMEM_COLS);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_s;
   const int total = tile_start_s[E];
-  const int W = gridDim.x;
+  const int W = gridDim.x >> 1;     // pairs
   const int katoms = args.K / 128;  // scale tiles along K
   const int nkb = (katoms + 1) / 2;
+  // the even CTA's full, tfree and unit_empty barriers, as shared::cluster addresses
+  const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+  const uint32_t tfree0 = mapa_shared(smem_u32(&tfree_bar[0]), 0);
+  const uint32_t uempty0 = mapa_shared(smem_u32(&unit_empty[0]), 0);
+
+  // A reader's next tile: wait for its slot, read it, free the slot for the
+  // producer (every reader frees every slot it reads, the end marker too).
+  // Returns total (the end) on a time-out.
+  auto next_unit = [&](int& uslot, uint32_t& uphase) -> int {
+    int u = total;
+    if (mbar_wait_cluster_bounded(&unit_full[uslot], uphase)) {
+      u = unit_ring[uslot];
+      mbar_arrive_cluster(uempty0 + uslot * 8u);
+    } else {
+      set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+      abort_s = 1;
+    }
+    if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
+    return u < total ? u : total;
+  };
+
+  // A wait of a whole converged warp: true in all lanes or false in all.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const bool ok = mbar_wait_cluster_bounded(bar, parity);
+    if (__all_sync(0xffffffffu, ok && !abort_s)) return true;
+    if (!ok) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+    abort_s = 1;
+    return false;
+  };
+  // next_unit for a whole warp (lane 0 reads); total once anything gave up.
+  auto next_unit_warp = [&](int& uslot, uint32_t& uphase) -> int {
+    int u = total;
+    if (lane == 0) {
+      u = next_unit(uslot, uphase);
+      if (abort_s) u = total;
+    } else if (++uslot == kUnitSlots) {
+      uslot = 0;
+      uphase ^= 1u;
+    }
+    return __shfl_sync(0xffffffffu, u, 0);
+  };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmB0);
       prefetch_tmap(&tmB1);
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t issued_mask = 0;  // stages that ever received a load
-      uint32_t last_parity = 0;  // parity of that stage's latest load
-      const int ngroups = args.N / 128;
-      for (int u = blockIdx.x; u < total && !abort_s; u += W) {
-        const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
-        const size_t ga = static_cast<size_t>(seg_s[t.e] / 128 + t.e + t.mt) * katoms;
-        const size_t gb = (static_cast<size_t>(t.e) * ngroups + t.n0 / 128) * katoms;
-        const int brow = t.e * args.N + t.n0;
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1u)) {
+      prefetch_tmap(&tmSA);
+      prefetch_tmap(&tmSB0);
+      prefetch_tmap(&tmSB1);
+    }
+    __syncwarp();
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t issued_mask = 0;  // stages that ever received a load
+    uint32_t last_parity = 0;  // parity of that stage's latest load
+    int uslot = 0;
+    uint32_t uphase = 0;
+    const int ngroups = args.N / 128;
+    const uint32_t ring_peer = mapa_shared(smem_u32(const_cast<int*>(&unit_ring[0])), 1);
+    const uint32_t ufull_peer = mapa_shared(smem_u32(&unit_full[0]), 1);
+    // The even CTA's lane 0 takes tiles one ahead: the counter's round trip
+    // overlaps the current tile's loads.
+    auto take = [&]() -> int {
+      return abort_s ? total
+                     : static_cast<int>(min(atomicAdd(&args.ctl->gemm_next, 1u), static_cast<unsigned>(total)));
+    };
+    int u_next = total;
+    if (rank == 0 && lane == 0) u_next = take();
+    for (;;) {
+      int u;
+      if (rank == 0) {
+        // publish the tile taken to both CTAs' readers
+        u = total;
+        if (lane == 0) {
+          if (mbar_wait_cluster_bounded(&unit_empty[uslot], uphase ^ 1u)) {
+            u = abort_s ? total : u_next;
+            if (u < total) u_next = take();
+            unit_ring[uslot] = u;
+            st_shared_cluster_u32(ring_peer + uslot * 4u, static_cast<uint32_t>(u));
+            mbar_arrive(&unit_full[uslot]);
+            mbar_arrive_cluster(ufull_peer + uslot * 8u);
+          } else {
             set_error(args.ctl, MOE_DEVERR_TIMEOUT);
             abort_s = 1;
-            break;
           }
-          uint8_t* sa = smem + stage * C::STAGE_BYTES;
-          uint8_t* ss = sa + C::OPERANDS;
-          uint64_t* fb = &full_bar[stage];
-          const uint32_t sbytes = min(2, katoms - 2 * kb) * kScaleTile;
-          mbar_arrive_expect_tx(fb, C::OPERANDS + (1 + C::NB) * sbytes);
-          tma_load_2d(sa, &tmA, fb, kb * 128, t.row0);
-          bulk_load(ss, args.sa + (ga + 2 * kb) * kScaleTile, sbytes, fb);
-#pragma unroll
-          for (int j = 0; j < C::NB; ++j) {
-            uint8_t* sb = sa + (1 + j) * kBoxBytes;
-            uint8_t* sj = ss + (1 + j) * 2 * kScaleTile;
-            if (EPI == EPI_SWIGLU) {
-              tma_load_2d(sb, j == 0 ? &tmB0 : &tmB1, fb, kb * 128, brow);
-              bulk_load(sj, (j == 0 ? args.sb0 : args.sb1) + (gb + 2 * kb) * kScaleTile, sbytes, fb);
-            } else {
-              tma_load_2d(sb, &tmB0, fb, kb * 128, brow + 128 * j);
-              bulk_load(sj, args.sb0 + (gb + static_cast<size_t>(j) * katoms + 2 * kb) * kScaleTile, sbytes, fb);
-            }
-          }
-          issued_mask |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
+      } else {
+        u = next_unit_warp(uslot, uphase);
       }
-      // Every load issued must have landed before the CTA may exit.
-      for (int s = 0; s < kStages; ++s)
-        if (issued_mask & (1u << s)) if (!mbar_wait_bounded(&full_bar[s], (last_parity >> s) & 1u)) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+      if (u >= total) break;
+      const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
+      const int arow = t.row0 + 128 * static_cast<int>(rank);
+      const int ga = (seg_s[t.e] / 128 + t.e + 2 * t.mt + static_cast<int>(rank)) * katoms;
+      const int gb = (t.e * ngroups + t.n0 / 128) * katoms;
+      // SwiGLU: CTA r loads matrix r's columns; otherwise CTA r its half
+      const CUtensorMap* mb = EPI == EPI_SWIGLU && rank == 1 ? &tmB1 : &tmB0;
+      const int brow = t.e * args.N + t.n0 + (EPI == EPI_SWIGLU ? 0 : C::B_ROWS * static_cast<int>(rank));
+      bool ok = true;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!warp_wait(&empty_bar[stage], phase ^ 1u)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * C::STAGE_BYTES;
+        uint8_t* ss = sa + C::OPERANDS;
+        const uint32_t fb = full0 + stage * 8u;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2u * C::STAGE_BYTES);
+          tma_load_2d_pair(sa, &tmA, fb, kb * 128, arow);
+          tma_load_2d_pair(sa + kBoxBytes, mb, fb, kb * 128, brow);
+          // two scale tiles each (the second is not used where K ends after one)
+          tma_load_2d_pair(ss, &tmSA, fb, 0, ga + 2 * kb);
+          tma_load_2d_pair(ss + 2 * kScaleTile, &tmSB0, fb, 0, gb + 2 * kb);
+          if (C::NB == 2)
+            tma_load_2d_pair(ss + 4 * kScaleTile, EPI == EPI_SWIGLU ? &tmSB1 : &tmSB0, fb, 0,
+                             (EPI == EPI_SWIGLU ? gb : gb + katoms) + 2 * kb);
+        }
+        __syncwarp();
+        issued_mask |= 1u << stage;
+        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+    }
+    // Every load issued must have been consumed by the MMAs (so it landed)
+    // before this CTA may leave: the MMA commit of each stage's last load
+    // arrives on empty[s] in both CTAs.
+    for (int s = 0; s < STAGES; ++s)
+      if (issued_mask & (1u << s))
+        if (!mbar_wait_bounded(&empty_bar[s], (last_parity >> s) & 1u)) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+    __syncwarp();
+    // The last pair to finish resets the tile counter for the next launch
+    // (every pair's last take precedes its increment here).
+    if (rank == 0 && lane == 0 && atomicAdd(&args.ctl->gemm_done, 1u) == static_cast<unsigned>(W) - 1u) {
+      atomicExch(&args.ctl->gemm_next, 0u);
+      atomicExch(&args.ctl->gemm_done, 0u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t kIdesc0 = make_idesc_mxf4(kTileM, NMMA, 0);
-      constexpr uint32_t kIdesc2 = make_idesc_mxf4(kTileM, NMMA, 2);
+    if (rank == 0) {
+      constexpr uint32_t kIdesc0 = make_idesc_mxf4(256, NMMA, 0);
+      constexpr uint32_t kIdesc2 = make_idesc_mxf4(256, NMMA, 2);
+      const uint32_t base = smem_u32(smem);
+      const uint64_t adesc0 = make_sw128_desc(base, 16, 1024);
+      const uint64_t bdesc0 = make_sw128_desc(base + kBoxBytes, 16, 1024);
+      const uint64_t sdesc0 = make_scale_desc(base + C::OPERANDS);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t set = 0;
-      int i = 0;  // tiles this CTA has started
       bool issued_any = false;
-      for (int u = blockIdx.x; u < total && !abort_s; u += W, ++i) {
-        // the previous tile's epilogue has read the columns shared with this
+      int uslot = 0;
+      uint32_t uphase = 0;
+      for (int i = 0;; ++i) {  // i: tiles this pair has started
+        const int u = next_unit_warp(uslot, uphase);
+        if (u >= total) break;
+        // the previous tile's epilogues have read the columns shared with this
         // tile's accumulator (and everything of the tile before it)
-        if (i > 0 && !mbar_wait_bounded(&tfree_bar[(i - 1) & 1], ((i - 1) >> 1) & 1)) {
-          set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-          abort_s = 1;
-          break;
-        }
+        if (i > 0 && !warp_wait(&tfree_bar[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + ((i & 1) ? C::ACC1 : 0);
         bool ok = true;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait_bounded(&full_bar[stage], phase)) {
-            set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-            abort_s = 1;
+          if (!warp_wait(&full_bar[stage], phase)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES);
-          const uint32_t b_addr = a_addr + kBoxBytes;
-          const uint32_t s_addr = a_addr + C::OPERANDS;
+          const uint32_t so = stage * (C::STAGE_BYTES >> 4);  // descriptors count 16 bytes
           const int atoms = min(2, katoms - 2 * kb);
-          for (int at = 0; at < atoms; ++at) {
-            const uint32_t sfa = tmem_base + C::SF_COL + set * 16;
-            const uint32_t sfb = sfa + 4;
-            copy_scales(sfa, s_addr + at * kScaleTile);
+          if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < C::NB; ++j)
-              copy_scales(sfb + 4 * j, s_addr + ((1 + j) * 2 + at) * kScaleTile);
+            for (int at = 0; at < 2; ++at) {
+              if (at < atoms) {
+                const uint32_t sfa = tmem_base + C::SF_COL + (set ^ at) * 16;
+                const uint32_t sfb = sfa + 4;
+                copy_scales(sfa, sdesc0 + so + at * (kScaleTile >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint32_t off = (at * 2 + kk) * 32;
-              umma_mxf4(d_tmem, make_sw128_desc(a_addr + off, 16, 1024), make_sw128_desc(b_addr + off, 16, 1024),
-                        kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb, (kb | at | kk) != 0 ? 1u : 0u);
+                for (int j = 0; j < C::NB; ++j)
+                  copy_scales(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                  const uint32_t off = so + (at * 2 + kk) * 2;
+                  umma_mxf4(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
+                            (kb | at | kk) != 0 ? 1u : 0u);
+                }
+              }
             }
-            set ^= 1u;
+            umma_commit_pair_mc(&empty_bar[stage], 0x3);
+            if (kb == nkb - 1) umma_commit_pair_mc(&tfull_bar[i & 1], 0x3);
           }
+          __syncwarp();
+          set ^= atoms & 1;
           issued_any = true;
-          umma_commit(&empty_bar[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        umma_commit(&tfull_bar[i & 1]);
       }
       if (issued_any) {
         // Tensor memory is freed below: wait until every MMA issued is done.
-        umma_commit(&drain_bar);
+        if (elect_one()) umma_commit_pair_mc(&drain_bar, 0x1);
+        __syncwarp();
         (void)mbar_wait_bounded(&drain_bar, 0);
       }
     }
   } else {
-    // epilogue warps 2..5: tensor-memory lane quarter = warp % 4
-    const int q = warp & 3;
-    int i = 0;
-    for (int u = blockIdx.x; u < total; u += W, ++i) {
+    // epilogue warps 2..9: tensor-memory lane quarter = warp % 4 of this CTA's
+    // 128 rows, first or second half of the column groups
+    constexpr int G = C::OUT_N / 64;  // groups of 32 columns per warp
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int uslot = 0;
+    uint32_t uphase = 0;
+    for (int i = 0;; ++i) {
       const int acc = i & 1;
       // Lane 0 polls and decides for the whole warp, so the warp-wide
       // tcgen05.ld below always runs converged.
-      int ok = 0;
+      int ok = 0, u = total;
       if (lane == 0) {
-        ok = !abort_s && mbar_wait_bounded(&tfull_bar[acc], (i >> 1) & 1);
-        if (!ok && !abort_s) {
+        u = next_unit(uslot, uphase);
+        ok = u < total && !abort_s && mbar_wait_cluster_bounded(&tfull_bar[acc], (i >> 1) & 1);
+        if (!ok && u < total && !abort_s) {
           set_error(args.ctl, MOE_DEVERR_TIMEOUT);
           abort_s = 1;
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      u = __shfl_sync(0xffffffffu, u, 0);
       tc_fence_after();
       const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc ? C::ACC1 : 0);
-      epilogue<EPI, C::OUT_N>(tbase, args, t, q * 32, lane, acc == 0 ? 1 : 0, [&] {
+      auto free_overlap = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tfree_bar[acc]);
-      });
+        if (lane == 0) mbar_arrive_cluster(tfree0 + acc * 8u);
+      };
+      // The shared columns are in the last group of the first accumulator
+      // (second half's warps) and in the first group of the second.
+      epilogue<EPI, C::OUT_N, G>(tbase, args, t, 128 * static_cast<int>(rank) + q * 32, lane, half * G, acc == 0,
+                                 free_overlap);
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // no peer still reads or signals this CTA; every MMA is done
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
   }
 }
 
@@ -408,18 +551,37 @@ bool make_tma_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t ro
   return r == CUDA_SUCCESS;
 }
 
+// Scale tiles [tiles, 512 bytes], box two tiles.
+bool make_tma_scales(CUtensorMap* m, const void* base, uint64_t tiles) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {kScaleTile / 4, tiles};
+  cuuint64_t strides[1] = {kScaleTile};
+  cuuint32_t box[2] = {kScaleTile / 4, 2};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 template <int EPI, int NMMA>
-cudaError_t run_gemm(const uint8_t* a, const uint8_t* b0, const uint8_t* b1, const MxArgs& args, cudaStream_t s) {
+cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
   using C = Cfg<EPI, NMMA>;
-  CUtensorMap ta, tb0, tb1;
-  const uint64_t brows = static_cast<uint64_t>(args.E) * args.N;
-  if (!make_tma_codes(&ta, a, static_cast<uint64_t>(args.rows_max), args.K / 2, 128) ||
-      !make_tma_codes(&tb0, b0, brows, args.K / 2, 128) ||
-      !make_tma_codes(&tb1, b1 != nullptr ? b1 : b0, brows, args.K / 2, 128))
+  CUtensorMap ta, tb0, tb1, sa, sb0, sb1;
+  const uint64_t brows = static_cast<uint64_t>(args.E) * args.N, katoms = args.K / 128;
+  const uint64_t atiles = (static_cast<uint64_t>(args.rows_max) / 128 + args.E) * katoms;
+  const MxWeights& up = EPI == EPI_SWIGLU ? b1 : b0;
+  if (!make_tma_codes(&ta, a.codes, static_cast<uint64_t>(args.rows_max), args.K / 2, 128) ||
+      !make_tma_codes(&tb0, b0.codes, brows, args.K / 2, C::B_ROWS) ||
+      !make_tma_codes(&tb1, up.codes, brows, args.K / 2, C::B_ROWS) ||
+      !make_tma_scales(&sa, a.scales, atiles) || !make_tma_scales(&sb0, b0.scales, brows / 128 * katoms) ||
+      !make_tma_scales(&sb1, up.scales, brows / 128 * katoms))
     return cudaErrorInvalidValue;
   auto kern = grouped_gemm_mxf4<EPI, NMMA>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
-  return launch_pdl(kern, dim3(num_sms()), dim3(kThreads), C::SMEM, s, false, ta, tb0, tb1, args);
+  const int pairs = num_sms() / 2;
+  return launch_pdl_cluster(kern, dim3(2 * pairs), dim3(kThreads), C::SMEM, s, 2, ta, tb0, tb1, sa, sb0, sb1, args);
 }
 
 }  // namespace
@@ -438,30 +600,24 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.E = E;
   a.rows_max = rows_max;
   a.ctl = ctl;
-  a.sa = x.scales;
-  a.sb0 = w1.scales;
-  a.sb1 = w3.scales;
   a.out_codes = h.codes;
   a.out_scales = h.scales;
   a.K = d;
   a.N = F;
   cudaError_t err;
   if (act == MOE_ACT_SWIGLU)
-    err = run_gemm<EPI_SWIGLU, 256>(x.codes, w1.codes, w3.codes, a, s);
+    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
   else if (F % 256 == 0)
-    err = run_gemm<EPI_GELU, 256>(x.codes, w1.codes, nullptr, a, s);
+    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
   else
-    err = run_gemm<EPI_GELU, 128>(x.codes, w1.codes, nullptr, a, s);
+    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, s);
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
-  a.sa = h.scales;
-  a.sb0 = w2.scales;
-  a.sb1 = nullptr;
   a.out = static_cast<__nv_bfloat16*>(y);
   a.K = F;
   a.N = d;
-  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h.codes, w2.codes, nullptr, a, s);
-  return run_gemm<EPI_STORE, 128>(h.codes, w2.codes, nullptr, a, s);
+  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
+  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
 }
 
 }  // namespace moe
