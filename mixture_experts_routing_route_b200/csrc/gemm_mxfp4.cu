@@ -33,9 +33,12 @@
 // next tile's MMAs start then, while the rest of the tile is still read.
 //
 // Work is handed out dynamically, as in the bf16 CTA-pair kernel: the even
-// CTA's producer takes the next tile from a counter in the control block and
-// publishes it to the pair's other roles, so that pairs sharing a weight block
-// read it at nearly the same time.
+// CTA's producer takes the next tile from a counter in the control block, so
+// that pairs sharing a weight block read it at nearly the same time. It hands
+// the tile to the odd CTA's producer, and each producer to its own CTA's roles.
+// Only the producers, which run ahead, wait with cluster scope: an acquire or
+// release at that scope stalled the MMA and epilogue warps by 2000 cycles each
+// time (measured), until their MMAs or stores in flight were done.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
 #include "gemm_common.cuh"
 #include "mxfp4.cuh"
@@ -52,10 +55,46 @@ constexpr int kTileM = 256;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (256 values of K)
 constexpr int kEpiWarps = 8;               // per CTA
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kUnitSlots = 4;              // ring of tiles published to the pair's roles
-constexpr uint32_t kUnitReaders = 2 + 2 * kEpiWarps;  // peer producer, MMA thread, epilogue warps
+constexpr int kUnitSlots = 4;              // ring of tiles published to a CTA's roles
 
 enum { EPI_SWIGLU = 0, EPI_GELU = 1, EPI_STORE = 2 };
+
+// Hardware exponential (base 2) and reciprocal, subnormals flushed: one
+// instruction each, within a few ulp.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The up projection's activations. Their result is rounded to E2M1, so a few
+// ulp never show; a tile has up to 32768 of them, and they bound the kernel
+// where K is short (with erff the epilogue of a 128 x 256 tile took 11500
+// cycles, the MMAs of K = 1024 2400).
+//
+// silu(g) = g / (1 + e^-g): for g < -128 ln 2 the exponential is Inf, its
+// reciprocal 0 and the result -0, the limit.
+__device__ __forceinline__ float silu_fast(float g) { return g * rcp(1.0f + ex2(-1.44269504f * g)); }
+
+// gelu(z) = z Phi(z) = max(z, 0) - |z| Phi(-|z|), Phi(-a) = erfc(a / sqrt 2) / 2
+// by Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26:
+// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), within 1.5e-7
+// (here the five coefficients are halved and p is divided by sqrt 2).
+__device__ __forceinline__ float gelu_fast(float z) {
+  const float a = fabsf(z);
+  const float t = rcp(fmaf(0.23164190f, a, 1.0f));
+  const float e = ex2(-0.72134752f * z * z);  // e^(-z^2 / 2)
+  float p = fmaf(0.5307027145f, t, -0.7265760135f);
+  p = fmaf(p, t, 0.7107068705f);
+  p = fmaf(p, t, -0.142248368f);
+  p = fmaf(p, t, 0.127414796f);
+  return fmaxf(z, 0.0f) - a * (p * t) * e;
+}
 
 struct MxArgs {
   const int32_t* seg;    // [E+1] row segment offsets
@@ -111,6 +150,12 @@ __device__ __forceinline__ uint64_t make_scale_desc(uint32_t smem_addr) {
 // four 32-lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Arrive on another CTA's mbarrier without a release: for arrivals that order
+// tensor-memory loads only (complete, and fenced by tcgen05.fence).
+__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 template <int EPI, int NMMA>
@@ -193,14 +238,14 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
       tmem_ld_wait();
       if (gi == 0) free_overlap();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) h[i] = silu(__uint_as_float(v[i])) * __uint_as_float(u[i]);
+      for (int i = 0; i < 32; ++i) h[i] = silu_fast(__uint_as_float(v[i])) * __uint_as_float(u[i]);
     } else {
       tmem_ld_32x32b_x32(tbase + 32 * g, v);
       tmem_ld_wait();
       if (gi == 0) free_overlap();
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        h[i] = EPI == EPI_GELU ? gelu_erf(__uint_as_float(v[i])) : __uint_as_float(v[i]);
+        h[i] = EPI == EPI_GELU ? gelu_fast(__uint_as_float(v[i])) : __uint_as_float(v[i]);
     }
     const int col = t.n0 + 32 * g;
     if constexpr (EPI == EPI_STORE) {
@@ -244,6 +289,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ __align__(8) uint64_t tfull_bar[2], tfree_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   __shared__ volatile int unit_ring[kUnitSlots];
+  // the even CTA's producer to the odd one's: full in the odd, empty in the even CTA
+  __shared__ __align__(8) uint64_t peer_full[kUnitSlots], peer_empty[kUnitSlots];
+  __shared__ volatile int peer_ring[kUnitSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int seg_s[kMaxE + 1];
   __shared__ int cnt_s[kMaxE];
@@ -269,7 +317,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * kEpiWarps); }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
-      mbar_init(&unit_empty[i], kUnitReaders);
+      mbar_init(&unit_empty[i], kEpiWarps + (rank == 0 ? 1 : 0));  // the readers: epilogue warps, MMA warp
+      mbar_init(&peer_full[i], 1);
+      mbar_init(&peer_empty[i], 1);
     }
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
@@ -286,19 +336,18 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   const int W = gridDim.x >> 1;     // pairs
   const int katoms = args.K / 128;  // scale tiles along K
   const int nkb = (katoms + 1) / 2;
-  // the even CTA's full, tfree and unit_empty barriers, as shared::cluster addresses
+  // the even CTA's full and tfree barriers, as shared::cluster addresses
   const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t tfree0 = mapa_shared(smem_u32(&tfree_bar[0]), 0);
-  const uint32_t uempty0 = mapa_shared(smem_u32(&unit_empty[0]), 0);
 
   // A reader's next tile: wait for its slot, read it, free the slot for the
   // producer (every reader frees every slot it reads, the end marker too).
   // Returns total (the end) on a time-out.
   auto next_unit = [&](int& uslot, uint32_t& uphase) -> int {
     int u = total;
-    if (mbar_wait_cluster_bounded(&unit_full[uslot], uphase)) {
+    if (mbar_wait_bounded(&unit_full[uslot], uphase)) {
       u = unit_ring[uslot];
-      mbar_arrive_cluster(uempty0 + uslot * 8u);
+      mbar_arrive(&unit_empty[uslot]);
     } else {
       set_error(args.ctl, MOE_DEVERR_TIMEOUT);
       abort_s = 1;
@@ -309,7 +358,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 
   // A wait of a whole converged warp: true in all lanes or false in all.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const bool ok = mbar_wait_cluster_bounded(bar, parity);
+    const bool ok = mbar_wait_bounded(bar, parity);
     if (__all_sync(0xffffffffu, ok && !abort_s)) return true;
     if (!ok) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
     abort_s = 1;
@@ -345,8 +394,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     int uslot = 0;
     uint32_t uphase = 0;
     const int ngroups = args.N / 128;
-    const uint32_t ring_peer = mapa_shared(smem_u32(const_cast<int*>(&unit_ring[0])), 1);
-    const uint32_t ufull_peer = mapa_shared(smem_u32(&unit_full[0]), 1);
+    const uint32_t pring1 = mapa_shared(smem_u32(const_cast<int*>(&peer_ring[0])), 1);
+    const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
+    const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
     // The even CTA's lane 0 takes tiles one ahead: the counter's round trip
     // overlaps the current tile's loads.
     auto take = [&]() -> int {
@@ -355,30 +405,45 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     };
     int u_next = total;
     if (rank == 0 && lane == 0) u_next = take();
-    for (;;) {
-      int u;
-      if (rank == 0) {
-        // publish the tile taken to both CTAs' readers
-        u = total;
-        if (lane == 0) {
-          if (mbar_wait_cluster_bounded(&unit_empty[uslot], uphase ^ 1u)) {
-            u = abort_s ? total : u_next;
-            if (u < total) u_next = take();
-            unit_ring[uslot] = u;
-            st_shared_cluster_u32(ring_peer + uslot * 4u, static_cast<uint32_t>(u));
-            mbar_arrive(&unit_full[uslot]);
-            mbar_arrive_cluster(ufull_peer + uslot * 8u);
-          } else {
-            set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-            abort_s = 1;
+    auto next_tile = [&]() -> int {
+      int u = total;
+      if (lane == 0) {
+        bool ok;
+        if (rank == 0) {  // hand the tile taken to the odd CTA's producer
+          ok = mbar_wait_cluster_bounded(&peer_empty[uslot], uphase ^ 1u);
+          u = ok && !abort_s ? u_next : total;
+          if (u < total) u_next = take();
+          if (ok) {
+            st_shared_cluster_u32(pring1 + uslot * 4u, static_cast<uint32_t>(u));
+            mbar_arrive_cluster(pfull1 + uslot * 8u);
           }
+        } else {
+          ok = mbar_wait_cluster_bounded(&peer_full[uslot], uphase);
+          u = ok && !abort_s ? peer_ring[uslot] : total;
+          if (ok) mbar_arrive_cluster(pempty0 + uslot * 8u);
         }
-        u = __shfl_sync(0xffffffffu, u, 0);
-        if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
-      } else {
-        u = next_unit_warp(uslot, uphase);
+        // and to this CTA's roles
+        if (mbar_wait_bounded(&unit_empty[uslot], uphase ^ 1u)) {
+          unit_ring[uslot] = u;
+          mbar_arrive(&unit_full[uslot]);
+        } else {
+          ok = false;
+        }
+        if (!ok) {
+          set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+          abort_s = 1;
+          u = total;
+        }
       }
-      if (u >= total) break;
+      if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
+      return __shfl_sync(0xffffffffu, u, 0);
+    };
+    // The next tile is handed over early in a tile, where the ring is full and
+    // the hand-over's latency costs nothing.
+    const int kb_next = min(2, nkb - 1);
+    int u = next_tile();
+    while (u < total) {
+      int u_after = total;
       const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
       const int arow = t.row0 + 128 * static_cast<int>(rank);
       const int ga = (seg_s[t.e] / 128 + t.e + 2 * t.mt + static_cast<int>(rank)) * katoms;
@@ -410,8 +475,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         issued_mask |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (kb == kb_next) u_after = next_tile();
       }
       if (!ok) break;
+      u = u_after;
     }
     // Every load issued must have been consumed by the MMAs (so it landed)
     // before this CTA may leave: the MMA commit of each stage's last load
@@ -506,7 +573,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       int ok = 0, u = total;
       if (lane == 0) {
         u = next_unit(uslot, uphase);
-        ok = u < total && !abort_s && mbar_wait_cluster_bounded(&tfull_bar[acc], (i >> 1) & 1);
+        ok = u < total && !abort_s && mbar_wait_bounded(&tfull_bar[acc], (i >> 1) & 1);
         if (!ok && u < total && !abort_s) {
           set_error(args.ctl, MOE_DEVERR_TIMEOUT);
           abort_s = 1;
@@ -520,7 +587,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       auto free_overlap = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tfree0 + acc * 8u);
+        if (lane == 0) arrive_relaxed_cluster(tfree0 + acc * 8u);
       };
       // The shared columns are in the last group of the first accumulator
       // (second half's warps) and in the first group of the second.
