@@ -173,11 +173,17 @@ struct Cfg {
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + 1024;
 };
 
-struct MxTile {
-  int e, mt, row0, rows, n0;
+struct __align__(16) MxTile {
+  int row0, rows, n0;
+  int group;  // row group (of 128) of its first row's scales
+  int e;
+  int pad[3];
 };
 
-// Tile u of the list: expert-major, then N tile, M tile fastest.
+// Tile u of the list: expert-major, then N tile, M tile fastest. The producers
+// decode it (some 1500 cycles of dependent reads and a division) and publish
+// the result: in the epilogue that time was spent between a full accumulator
+// and its first read.
 __device__ __forceinline__ MxTile decode_tile(int u, const int* tile_start, const int* seg, const int* cnt,
                                               int E, int out_n) {
   int lo = 0, hi = E - 1;  // last e with tile_start[e] <= u
@@ -189,11 +195,11 @@ __device__ __forceinline__ MxTile decode_tile(int u, const int* tile_start, cons
   t.e = lo;
   const int mt_e = (cnt[lo] + kTileM - 1) / kTileM;
   const int local = u - tile_start[lo];
-  const int nt = local / mt_e;
-  t.mt = local - nt * mt_e;
-  t.row0 = seg[lo] + t.mt * kTileM;
-  t.rows = min(kTileM, cnt[lo] - t.mt * kTileM);
+  const int nt = local / mt_e, mt = local - nt * mt_e;
+  t.row0 = seg[lo] + mt * kTileM;
+  t.rows = min(kTileM, cnt[lo] - mt * kTileM);
   t.n0 = nt * out_n;
+  t.group = seg[lo] / 128 + lo + mt * (kTileM / 128);
   return t;
 }
 
@@ -265,10 +271,8 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
   }
   if constexpr (EPI != EPI_STORE) {
     if (valid) {
-      // this warp's rows lie in one group of 128 of the expert's rows
-      const int r = t.mt * kTileM + crow + lane;
-      const long long group = (t.row0 - t.mt * kTileM) / 128 + t.e + r / 128;
-      uint8_t* dst = args.out_scales + mx_scale_at(group, args.N / 128, r & 127, t.n0 / 32 + g0);
+      const int r = crow + lane;
+      uint8_t* dst = args.out_scales + mx_scale_at(t.group + r / 128, args.N / 128, r & 127, t.n0 / 32 + g0);
       static_assert(G == 2 || G == 4, "half of 128 or of 256 columns");
       if constexpr (G == 4) *reinterpret_cast<uint32_t*>(dst) = sw;
       else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sw);
@@ -288,7 +292,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2], tfree_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
-  __shared__ volatile int unit_ring[kUnitSlots];
+  __shared__ MxTile unit_ring[kUnitSlots];  // rows = 0: the end
   // the even CTA's producer to the odd one's: full in the odd, empty in the even CTA
   __shared__ __align__(8) uint64_t peer_full[kUnitSlots], peer_empty[kUnitSlots];
   __shared__ volatile int peer_ring[kUnitSlots];
@@ -340,43 +344,31 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t tfree0 = mapa_shared(smem_u32(&tfree_bar[0]), 0);
 
-  // A reader's next tile: wait for its slot, read it, free the slot for the
-  // producer (every reader frees every slot it reads, the end marker too).
-  // Returns total (the end) on a time-out.
-  auto next_unit = [&](int& uslot, uint32_t& uphase) -> int {
-    int u = total;
-    if (mbar_wait_bounded(&unit_full[uslot], uphase)) {
-      u = unit_ring[uslot];
-      mbar_arrive(&unit_empty[uslot]);
-    } else {
+  // A reader's next tile, by a whole converged warp: wait for its slot, read it
+  // and free it for the producer (every reader frees every slot it reads, the
+  // end marker too). False at the end, and once anything gave up.
+  auto next_unit = [&](int& uslot, uint32_t& uphase, MxTile& t) -> bool {
+    const bool ok = mbar_wait_bounded(&unit_full[uslot], uphase);
+    if (!__all_sync(0xffffffffu, ok)) {
       set_error(args.ctl, MOE_DEVERR_TIMEOUT);
       abort_s = 1;
+      return false;
     }
+    t = unit_ring[uslot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&unit_empty[uslot]);
     if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
-    return u < total ? u : total;
+    return t.rows > 0;
   };
 
   // A wait of a whole converged warp: true in all lanes or false in all.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     const bool ok = mbar_wait_bounded(bar, parity);
-    if (__all_sync(0xffffffffu, ok && !abort_s)) return true;
+    if (__all_sync(0xffffffffu, ok)) return true;
     if (!ok) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
     abort_s = 1;
     return false;
   };
-  // next_unit for a whole warp (lane 0 reads); total once anything gave up.
-  auto next_unit_warp = [&](int& uslot, uint32_t& uphase) -> int {
-    int u = total;
-    if (lane == 0) {
-      u = next_unit(uslot, uphase);
-      if (abort_s) u = total;
-    } else if (++uslot == kUnitSlots) {
-      uslot = 0;
-      uphase ^= 1u;
-    }
-    return __shfl_sync(0xffffffffu, u, 0);
-  };
-
   if (warp == 0) {
     if (elect_one()) {
       prefetch_tmap(&tmA);
@@ -405,10 +397,11 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     };
     int u_next = total;
     if (rank == 0 && lane == 0) u_next = take();
-    auto next_tile = [&]() -> int {
-      int u = total;
+    auto next_tile = [&]() -> MxTile {
+      MxTile t{};
       if (lane == 0) {
         bool ok;
+        int u;
         if (rank == 0) {  // hand the tile taken to the odd CTA's producer
           ok = mbar_wait_cluster_bounded(&peer_empty[uslot], uphase ^ 1u);
           u = ok && !abort_s ? u_next : total;
@@ -422,9 +415,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
           u = ok && !abort_s ? peer_ring[uslot] : total;
           if (ok) mbar_arrive_cluster(pempty0 + uslot * 8u);
         }
+        if (u < total) t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
         // and to this CTA's roles
         if (mbar_wait_bounded(&unit_empty[uslot], uphase ^ 1u)) {
-          unit_ring[uslot] = u;
+          unit_ring[uslot] = t;
           mbar_arrive(&unit_full[uslot]);
         } else {
           ok = false;
@@ -432,21 +426,25 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         if (!ok) {
           set_error(args.ctl, MOE_DEVERR_TIMEOUT);
           abort_s = 1;
-          u = total;
+          t.rows = 0;
         }
       }
       if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
-      return __shfl_sync(0xffffffffu, u, 0);
+      t.row0 = __shfl_sync(0xffffffffu, t.row0, 0);
+      t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+      t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
+      t.group = __shfl_sync(0xffffffffu, t.group, 0);
+      t.e = __shfl_sync(0xffffffffu, t.e, 0);
+      return t;
     };
     // The next tile is handed over early in a tile, where the ring is full and
     // the hand-over's latency costs nothing.
     const int kb_next = min(2, nkb - 1);
-    int u = next_tile();
-    while (u < total) {
-      int u_after = total;
-      const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
+    MxTile t = next_tile();
+    while (t.rows > 0) {
+      MxTile t_after{};
       const int arow = t.row0 + 128 * static_cast<int>(rank);
-      const int ga = (seg_s[t.e] / 128 + t.e + 2 * t.mt + static_cast<int>(rank)) * katoms;
+      const int ga = (t.group + static_cast<int>(rank)) * katoms;
       const int gb = (t.e * ngroups + t.n0 / 128) * katoms;
       // SwiGLU: CTA r loads matrix r's columns; otherwise CTA r its half
       const CUtensorMap* mb = EPI == EPI_SWIGLU && rank == 1 ? &tmB1 : &tmB0;
@@ -475,10 +473,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         issued_mask |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        if (kb == kb_next) u_after = next_tile();
+        if (kb == kb_next) t_after = next_tile();
       }
       if (!ok) break;
-      u = u_after;
+      t = t_after;
     }
     // Every load issued must have been consumed by the MMAs (so it landed)
     // before this CTA may leave: the MMA commit of each stage's last load
@@ -508,16 +506,18 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       int uslot = 0;
       uint32_t uphase = 0;
       for (int i = 0;; ++i) {  // i: tiles this pair has started
-        const int u = next_unit_warp(uslot, uphase);
-        if (u >= total) break;
-        // the previous tile's epilogues have read the columns shared with this
-        // tile's accumulator (and everything of the tile before it)
+        MxTile t;
+        if (!next_unit(uslot, uphase, t)) break;
+        // the first stage has landed, and the previous tile's epilogues have read
+        // the columns shared with this tile's accumulator (and everything of the
+        // tile before it)
+        if (!warp_wait(&full_bar[stage], phase)) break;
         if (i > 0 && !warp_wait(&tfree_bar[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + ((i & 1) ? C::ACC1 : 0);
         bool ok = true;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!warp_wait(&full_bar[stage], phase)) {
+          if (kb > 0 && !warp_wait(&full_bar[stage], phase)) {
             ok = false;
             break;
           }
@@ -568,21 +568,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     uint32_t uphase = 0;
     for (int i = 0;; ++i) {
       const int acc = i & 1;
-      // Lane 0 polls and decides for the whole warp, so the warp-wide
-      // tcgen05.ld below always runs converged.
-      int ok = 0, u = total;
-      if (lane == 0) {
-        u = next_unit(uslot, uphase);
-        ok = u < total && !abort_s && mbar_wait_bounded(&tfull_bar[acc], (i >> 1) & 1);
-        if (!ok && u < total && !abort_s) {
-          set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-          abort_s = 1;
-        }
-      }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      u = __shfl_sync(0xffffffffu, u, 0);
+      MxTile t;
+      if (!next_unit(uslot, uphase, t) || !warp_wait(&tfull_bar[acc], (i >> 1) & 1)) break;
       tc_fence_after();
-      const MxTile t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (acc ? C::ACC1 : 0);
       auto free_overlap = [&] {
         tc_fence_before();
