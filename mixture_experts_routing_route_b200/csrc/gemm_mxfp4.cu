@@ -12,7 +12,7 @@
 // The two CTAs of a cluster compute one 256-row x N tile together
 // (cta_group::2), persistently. CTA r holds A rows [row0 + 128 r, +128) and its
 // half of the B columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output
-// columns), its rows' scales and the scales of all B columns. Ten warps a CTA:
+// columns), its rows' scales and the scales of all B columns. Eleven warps a CTA:
 //   warp 0   producer: per stage (256 values of K) the A and B boxes by TMA (128
 //            bytes = 256 codes a row, 128-byte swizzle) and the scale tiles (two
 //            of 512 bytes per 128 rows)
@@ -32,13 +32,16 @@
 // epilogue reads the overlapping columns first and frees them at once; the
 // next tile's MMAs start then, while the rest of the tile is still read.
 //
-// Work is handed out dynamically, as in the bf16 CTA-pair kernel: the even
-// CTA's producer takes the next tile from a counter in the control block, so
-// that pairs sharing a weight block read it at nearly the same time. It hands
-// the tile to the odd CTA's producer, and each producer to its own CTA's roles.
-// Only the producers, which run ahead, wait with cluster scope: an acquire or
-// release at that scope stalled the MMA and epilogue warps by 2000 cycles each
-// time (measured), until their MMAs or stores in flight were done.
+//   warp 10  scheduler: hands out tiles
+//
+// Work is handed out dynamically, as in the bf16 CTA-pair kernel, so that pairs
+// sharing a weight block read it at nearly the same time: the even CTA's
+// scheduler takes the next tile from a counter in the control block, decodes
+// it, publishes it to its CTA's roles and hands it to the odd CTA's scheduler,
+// which does the same there. The three-slot ring keeps this chain (some 3000
+// cycles a tile: the counter, a search with a division, waits and releases at
+// cluster scope) off every other role's path, and takes no tile so early that
+// a slow pair would hold work an idle one could do.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
 #include "gemm_common.cuh"
 #include "mxfp4.cuh"
@@ -54,8 +57,9 @@ namespace {
 constexpr int kTileM = 256;
 constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (256 values of K)
 constexpr int kEpiWarps = 8;               // per CTA
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kUnitSlots = 4;              // ring of tiles published to a CTA's roles
+constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
+constexpr int kUnitSlots = 3;              // ring of tiles published to a CTA's roles
+constexpr uint32_t kUnitReaders = 1 + kEpiWarps;  // producer, epilogue warps (and the even CTA's MMA warp)
 
 enum { EPI_SWIGLU = 0, EPI_GELU = 1, EPI_STORE = 2 };
 
@@ -180,10 +184,7 @@ struct __align__(16) MxTile {
   int pad[3];
 };
 
-// Tile u of the list: expert-major, then N tile, M tile fastest. The producers
-// decode it (some 1500 cycles of dependent reads and a division) and publish
-// the result: in the epilogue that time was spent between a full accumulator
-// and its first read.
+// Tile u of the list: expert-major, then N tile, M tile fastest.
 __device__ __forceinline__ MxTile decode_tile(int u, const int* tile_start, const int* seg, const int* cnt,
                                               int E, int out_n) {
   int lo = 0, hi = E - 1;  // last e with tile_start[e] <= u
@@ -285,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmSA,
                   const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1, MxArgs args) {
-  pdl_begin();
   using C = Cfg<EPI, NMMA>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -293,9 +293,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ __align__(8) uint64_t tfull_bar[2], tfree_bar[2], drain_bar;
   __shared__ __align__(8) uint64_t unit_full[kUnitSlots], unit_empty[kUnitSlots];
   __shared__ MxTile unit_ring[kUnitSlots];  // rows = 0: the end
-  // the even CTA's producer to the odd one's: full in the odd, empty in the even CTA
+  // the even CTA's scheduler to the odd one's: full in the odd, empty in the even CTA
   __shared__ __align__(8) uint64_t peer_full[kUnitSlots], peer_empty[kUnitSlots];
-  __shared__ volatile int peer_ring[kUnitSlots];
+  __shared__ MxTile peer_ring[kUnitSlots];
   __shared__ uint32_t tmem_base_s;
   __shared__ int seg_s[kMaxE + 1];
   __shared__ int cnt_s[kMaxE];
@@ -303,40 +303,48 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ volatile int abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = args.E;
   const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the MMAs
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
 
-  for (int i = threadIdx.x; i <= E; i += kThreads) {
-    seg_s[i] = __ldg(args.seg + i);
-    if (i < E)
-      cnt_s[i] = args.kept != nullptr ? __ldg(args.kept + i) : __ldg(args.seg + i + 1) - __ldg(args.seg + i);
-  }
-  if (threadIdx.x == 0) abort_s = 0;
-  __syncthreads();
-  if (warp == 0) build_schedule<kTileM>(args, args.N / C::OUT_N, seg_s, cnt_s, tile_start_s, lane);
+  // Set-up that needs nothing of the kernel before this one, so that it runs
+  // under that kernel's tail.
   if (threadIdx.x == 0) {
+    abort_s = 0;
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
     for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * kEpiWarps); }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
-      mbar_init(&unit_empty[i], kEpiWarps + (rank == 0 ? 1 : 0));  // the readers: epilogue warps, MMA warp
+      mbar_init(&unit_empty[i], kUnitReaders + (rank == 0 ? 1 : 0));
       mbar_init(&peer_full[i], 1);
       mbar_init(&peer_empty[i], 1);
     }
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == 1) {
     tmem_alloc_pair(&tmem_base_s, C::TMEM_COLS);
     tmem_relinquish_pair();
+  }
+  if (warp == 10 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB0);
+    prefetch_tmap(&tmB1);
+    prefetch_tmap(&tmSA);
+    prefetch_tmap(&tmSB0);
+    prefetch_tmap(&tmSB1);
   }
   tc_fence_before();
   cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
   tc_fence_after();
-  const uint32_t tmem_base = tmem_base_s;
-  const int total = tile_start_s[E];
+  pdl_begin();
+  // All 512 columns are this CTA's, so they start at 0: addresses below are
+  // constants (a loaded base would go through registers at every instruction).
+  if (tmem_base_s != 0 && threadIdx.x == 0) {
+    set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+    abort_s = 1;
+  }
+  constexpr uint32_t tmem_base = 0;
   const int W = gridDim.x >> 1;     // pairs
   const int katoms = args.K / 128;  // scale tiles along K
   const int nkb = (katoms + 1) / 2;
@@ -344,16 +352,22 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
   const uint32_t tfree0 = mapa_shared(smem_u32(&tfree_bar[0]), 0);
 
+  auto give_up = [&] {
+    set_error(args.ctl, MOE_DEVERR_TIMEOUT);
+    abort_s = 1;
+  };
+  // A wait of a whole converged warp: true in all lanes or false in all.
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const bool ok = mbar_wait_bounded(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    give_up();
+    return false;
+  };
   // A reader's next tile, by a whole converged warp: wait for its slot, read it
-  // and free it for the producer (every reader frees every slot it reads, the
-  // end marker too). False at the end, and once anything gave up.
+  // and free it (every reader frees every slot it reads, the end marker too).
+  // False at the end, and once anything gave up.
   auto next_unit = [&](int& uslot, uint32_t& uphase, MxTile& t) -> bool {
-    const bool ok = mbar_wait_bounded(&unit_full[uslot], uphase);
-    if (!__all_sync(0xffffffffu, ok)) {
-      set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-      abort_s = 1;
-      return false;
-    }
+    if (!warp_wait(&unit_full[uslot], uphase)) return false;
     t = unit_ring[uslot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&unit_empty[uslot]);
@@ -361,24 +375,68 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     return t.rows > 0;
   };
 
-  // A wait of a whole converged warp: true in all lanes or false in all.
-  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    const bool ok = mbar_wait_bounded(bar, parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if (!ok) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-    abort_s = 1;
-    return false;
-  };
-  if (warp == 0) {
-    if (elect_one()) {
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB0);
-      prefetch_tmap(&tmB1);
-      prefetch_tmap(&tmSA);
-      prefetch_tmap(&tmSB0);
-      prefetch_tmap(&tmSB1);
+  if (warp == 10) {
+    int total = 0;
+    if (rank == 0) {
+      // the list of tiles: row segments, and each expert's first tile
+      for (int i = lane; i <= args.E; i += 32) {
+        seg_s[i] = __ldg(args.seg + i);
+        if (i < args.E)
+          cnt_s[i] = args.kept != nullptr ? __ldg(args.kept + i) : __ldg(args.seg + i + 1) - __ldg(args.seg + i);
+      }
+      __syncwarp();
+      build_schedule<kTileM>(args, args.N / C::OUT_N, seg_s, cnt_s, tile_start_s, lane);
+      __syncwarp();
+      total = tile_start_s[args.E];
     }
-    __syncwarp();
+    if (lane == 0) {
+      const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
+      const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
+      const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
+      int slot = 0;
+      uint32_t phase = 0;
+      for (;;) {
+        MxTile t{};
+        // a slot is free here once every role of this CTA has read it; the odd
+        // CTA frees its copy once it has taken it over
+        bool ok = mbar_wait_bounded(&unit_empty[slot], phase ^ 1u);
+        if (rank == 0) {
+          ok = ok && mbar_wait_cluster_bounded(&peer_empty[slot], phase ^ 1u);
+          if (ok && !abort_s) {
+            const int u = static_cast<int>(min(atomicAdd(&args.ctl->gemm_next, 1u), static_cast<unsigned>(total)));
+            if (u < total) t = decode_tile(u, tile_start_s, seg_s, cnt_s, args.E, C::OUT_N);
+          }
+          if (ok) {
+            const uint32_t dst = pring1 + slot * static_cast<uint32_t>(sizeof(MxTile));
+            st_shared_cluster_u32(dst, static_cast<uint32_t>(t.row0));
+            st_shared_cluster_u32(dst + 4, static_cast<uint32_t>(t.rows));
+            st_shared_cluster_u32(dst + 8, static_cast<uint32_t>(t.n0));
+            st_shared_cluster_u32(dst + 12, static_cast<uint32_t>(t.group));
+            st_shared_cluster_u32(dst + 16, static_cast<uint32_t>(t.e));
+            mbar_arrive_cluster(pfull1 + slot * 8u);
+          }
+        } else {
+          ok = ok && mbar_wait_cluster_bounded(&peer_full[slot], phase);
+          if (ok) {
+            t = *const_cast<const MxTile*>(&peer_ring[slot]);
+            mbar_arrive_cluster(pempty0 + slot * 8u);
+          }
+        }
+        if (!ok) give_up();
+        if (!ok || abort_s) t.rows = 0;
+        unit_ring[slot] = t;
+        mbar_arrive(&unit_full[slot]);
+        if (++slot == kUnitSlots) { slot = 0; phase ^= 1u; }
+        if (t.rows == 0) break;
+      }
+      // The last pair to finish resets the tile counter for the next launch
+      // (every pair's last take precedes its increment here).
+      if (rank == 0 && atomicAdd(&args.ctl->gemm_done, 1u) == static_cast<unsigned>(W) - 1u) {
+        atomicExch(&args.ctl->gemm_next, 0u);
+        atomicExch(&args.ctl->gemm_done, 0u);
+      }
+    }
+  } else if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
     uint32_t issued_mask = 0;  // stages that ever received a load
@@ -386,70 +444,15 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     int uslot = 0;
     uint32_t uphase = 0;
     const int ngroups = args.N / 128;
-    const uint32_t pring1 = mapa_shared(smem_u32(const_cast<int*>(&peer_ring[0])), 1);
-    const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
-    const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
-    // The even CTA's lane 0 takes tiles one ahead: the counter's round trip
-    // overlaps the current tile's loads.
-    auto take = [&]() -> int {
-      return abort_s ? total
-                     : static_cast<int>(min(atomicAdd(&args.ctl->gemm_next, 1u), static_cast<unsigned>(total)));
-    };
-    int u_next = total;
-    if (rank == 0 && lane == 0) u_next = take();
-    auto next_tile = [&]() -> MxTile {
-      MxTile t{};
-      if (lane == 0) {
-        bool ok;
-        int u;
-        if (rank == 0) {  // hand the tile taken to the odd CTA's producer
-          ok = mbar_wait_cluster_bounded(&peer_empty[uslot], uphase ^ 1u);
-          u = ok && !abort_s ? u_next : total;
-          if (u < total) u_next = take();
-          if (ok) {
-            st_shared_cluster_u32(pring1 + uslot * 4u, static_cast<uint32_t>(u));
-            mbar_arrive_cluster(pfull1 + uslot * 8u);
-          }
-        } else {
-          ok = mbar_wait_cluster_bounded(&peer_full[uslot], uphase);
-          u = ok && !abort_s ? peer_ring[uslot] : total;
-          if (ok) mbar_arrive_cluster(pempty0 + uslot * 8u);
-        }
-        if (u < total) t = decode_tile(u, tile_start_s, seg_s, cnt_s, E, C::OUT_N);
-        // and to this CTA's roles
-        if (mbar_wait_bounded(&unit_empty[uslot], uphase ^ 1u)) {
-          unit_ring[uslot] = t;
-          mbar_arrive(&unit_full[uslot]);
-        } else {
-          ok = false;
-        }
-        if (!ok) {
-          set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-          abort_s = 1;
-          t.rows = 0;
-        }
-      }
-      if (++uslot == kUnitSlots) { uslot = 0; uphase ^= 1u; }
-      t.row0 = __shfl_sync(0xffffffffu, t.row0, 0);
-      t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
-      t.n0 = __shfl_sync(0xffffffffu, t.n0, 0);
-      t.group = __shfl_sync(0xffffffffu, t.group, 0);
-      t.e = __shfl_sync(0xffffffffu, t.e, 0);
-      return t;
-    };
-    // The next tile is handed over early in a tile, where the ring is full and
-    // the hand-over's latency costs nothing.
-    const int kb_next = min(2, nkb - 1);
-    MxTile t = next_tile();
-    while (t.rows > 0) {
-      MxTile t_after{};
+    MxTile t;
+    bool ok = true;
+    while (ok && next_unit(uslot, uphase, t)) {
       const int arow = t.row0 + 128 * static_cast<int>(rank);
       const int ga = (t.group + static_cast<int>(rank)) * katoms;
       const int gb = (t.e * ngroups + t.n0 / 128) * katoms;
       // SwiGLU: CTA r loads matrix r's columns; otherwise CTA r its half
       const CUtensorMap* mb = EPI == EPI_SWIGLU && rank == 1 ? &tmB1 : &tmB0;
       const int brow = t.e * args.N + t.n0 + (EPI == EPI_SWIGLU ? 0 : C::B_ROWS * static_cast<int>(rank));
-      bool ok = true;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!warp_wait(&empty_bar[stage], phase ^ 1u)) {
           ok = false;
@@ -473,10 +476,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         issued_mask |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        if (kb == kb_next) t_after = next_tile();
       }
-      if (!ok) break;
-      t = t_after;
     }
     // Every load issued must have been consumed by the MMAs (so it landed)
     // before this CTA may leave: the MMA commit of each stage's last load
@@ -484,13 +484,6 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     for (int s = 0; s < STAGES; ++s)
       if (issued_mask & (1u << s))
         if (!mbar_wait_bounded(&empty_bar[s], (last_parity >> s) & 1u)) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
-    __syncwarp();
-    // The last pair to finish resets the tile counter for the next launch
-    // (every pair's last take precedes its increment here).
-    if (rank == 0 && lane == 0 && atomicAdd(&args.ctl->gemm_done, 1u) == static_cast<unsigned>(W) - 1u) {
-      atomicExch(&args.ctl->gemm_next, 0u);
-      atomicExch(&args.ctl->gemm_done, 0u);
-    }
   } else if (warp == 1) {
     if (rank == 0) {
       constexpr uint32_t kIdesc0 = make_idesc_mxf4(256, NMMA, 0);
@@ -502,57 +495,55 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       int stage = 0;
       uint32_t phase = 0;
       uint32_t set = 0;
-      bool issued_any = false;
+      bool issued_any = false, dead = false;  // in the issuing thread
       int uslot = 0;
       uint32_t uphase = 0;
       for (int i = 0;; ++i) {  // i: tiles this pair has started
         MxTile t;
         if (!next_unit(uslot, uphase, t)) break;
-        // the first stage has landed, and the previous tile's epilogues have read
-        // the columns shared with this tile's accumulator (and everything of the
-        // tile before it)
-        if (!warp_wait(&full_bar[stage], phase)) break;
-        if (i > 0 && !warp_wait(&tfree_bar[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + ((i & 1) ? C::ACC1 : 0);
-        bool ok = true;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (kb > 0 && !warp_wait(&full_bar[stage], phase)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
           const uint32_t so = stage * (C::STAGE_BYTES >> 4);  // descriptors count 16 bytes
           const int atoms = min(2, katoms - 2 * kb);
           if (elect_one()) {
+            if (!dead) dead = !mbar_wait_bounded(&full_bar[stage], phase);
+            // the previous tile's epilogues have read the columns shared with
+            // this tile's accumulator (and everything of the tile before it)
+            if (kb == 0 && i > 0 && !dead) dead = !mbar_wait_bounded(&tfree_bar[(i - 1) & 1], ((i - 1) >> 1) & 1);
+            if (!dead) {
+              tc_fence_after();
 #pragma unroll
-            for (int at = 0; at < 2; ++at) {
-              if (at < atoms) {
-                const uint32_t sfa = tmem_base + C::SF_COL + (set ^ at) * 16;
-                const uint32_t sfb = sfa + 4;
-                copy_scales(sfa, sdesc0 + so + at * (kScaleTile >> 4));
+              for (int at = 0; at < 2; ++at) {
+                if (at < atoms) {
+                  const uint32_t sfa = tmem_base + C::SF_COL + (set ^ at) * 16;
+                  const uint32_t sfb = sfa + 4;
+                  copy_scales(sfa, sdesc0 + so + at * (kScaleTile >> 4));
 #pragma unroll
-                for (int j = 0; j < C::NB; ++j)
-                  copy_scales(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
+                  for (int j = 0; j < C::NB; ++j)
+                    copy_scales(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                  const uint32_t off = so + (at * 2 + kk) * 2;
-                  umma_mxf4(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
-                            (kb | at | kk) != 0 ? 1u : 0u);
+                  for (int kk = 0; kk < 2; ++kk) {
+                    const uint32_t off = so + (at * 2 + kk) * 2;
+                    umma_mxf4(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
+                              (kb | at | kk) != 0 ? 1u : 0u);
+                  }
                 }
               }
+              umma_commit_pair_mc(&empty_bar[stage], 0x3);
+              if (kb == nkb - 1) umma_commit_pair_mc(&tfull_bar[i & 1], 0x3);
+              issued_any = true;
             }
-            umma_commit_pair_mc(&empty_bar[stage], 0x3);
-            if (kb == nkb - 1) umma_commit_pair_mc(&tfull_bar[i & 1], 0x3);
           }
           __syncwarp();
           set ^= atoms & 1;
-          issued_any = true;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (!ok) break;
+        if (__any_sync(0xffffffffu, dead)) {
+          give_up();
+          break;
+        }
       }
-      if (issued_any) {
+      if (__any_sync(0xffffffffu, issued_any)) {
         // Tensor memory is freed below: wait until every MMA issued is done.
         if (elect_one()) umma_commit_pair_mc(&drain_bar, 0x1);
         __syncwarp();
@@ -586,9 +577,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no peer still reads or signals this CTA; every MMA is done
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base_s, C::TMEM_COLS);
   }
 }
 
