@@ -109,6 +109,7 @@ struct MxArgs {
   int E;
   int K;
   int N;  // output columns
+  int early;  // seg, kept and the weights were complete before the previous kernel on the stream began
   long long rows_max;
   Control* ctl;
 };
@@ -184,25 +185,72 @@ struct __align__(16) MxTile {
   int pad[3];
 };
 
-// Tile u of the list: expert-major, then N tile, M tile fastest.
-__device__ __forceinline__ MxTile decode_tile(int u, const int* tile_start, const int* seg, const int* cnt,
-                                              int E, int out_n) {
-  int lo = 0, hi = E - 1;  // last e with tile_start[e] <= u
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tile_start[mid] <= u) lo = mid; else hi = mid - 1;
+// The list of tiles, held by one warp: lane l has experts [8 l, 8 l + 8) with
+// their first rows, row counts and first tiles. Tiles are ordered
+// expert-major, then N tile, M tile fastest.
+struct TileList {
+  int seg[8], cnt[8], start[8];
+  int total;
+
+  __device__ __forceinline__ void build(const MxArgs& args, int ntn, int lane) {
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane * 8 + i;
+      seg[i] = cnt[i] = 0;
+      int end = 0;
+      if (e < args.E) {
+        seg[i] = __ldg(args.seg + e);
+        end = __ldg(args.seg + e + 1);
+        cnt[i] = args.kept != nullptr ? __ldg(args.kept + e) : end - seg[i];
+      }
+      // rows out of range are reported and their expert gets no tiles
+      if (cnt[i] < 0 || seg[i] < 0 || static_cast<long long>(seg[i]) + cnt[i] > min(args.rows_max, static_cast<long long>(end))) {
+        set_error(args.ctl, MOE_DEVERR_ROW_RANGE);
+        cnt[i] = 0;
+      }
+      start[i] = ((cnt[i] + kTileM - 1) / kTileM) * ntn;
+      sum += start[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += n;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    int run = incl - sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n = start[i];
+      start[i] = run;
+      run += n;
+    }
   }
-  MxTile t;
-  t.e = lo;
-  const int mt_e = (cnt[lo] + kTileM - 1) / kTileM;
-  const int local = u - tile_start[lo];
-  const int nt = local / mt_e, mt = local - nt * mt_e;
-  t.row0 = seg[lo] + mt * kTileM;
-  t.rows = min(kTileM, cnt[lo] - mt * kTileM);
-  t.n0 = nt * out_n;
-  t.group = seg[lo] / 128 + lo + mt * (kTileM / 128);
-  return t;
-}
+
+  // Tile u < total, by the whole warp.
+  __device__ __forceinline__ MxTile tile(int u, int out_n, int lane) const {
+    int s = -1, c = 0, st = 0, e = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (start[i] <= u) { s = seg[i]; c = cnt[i]; st = start[i]; e = lane * 8 + i; }
+    // the last lane with an expert that starts at or before u
+    const int src = 31 - __clz(__ballot_sync(0xffffffffu, s >= 0));
+    s = __shfl_sync(0xffffffffu, s, src);
+    c = __shfl_sync(0xffffffffu, c, src);
+    st = __shfl_sync(0xffffffffu, st, src);
+    MxTile t;
+    t.e = __shfl_sync(0xffffffffu, e, src);
+    const int mt_e = (c + kTileM - 1) / kTileM;
+    const int local = u - st;
+    const int nt = local / mt_e, mt = local - nt * mt_e;
+    t.row0 = s + mt * kTileM;
+    t.rows = min(kTileM, c - mt * kTileM);
+    t.n0 = nt * out_n;
+    t.group = s / 128 + t.e + mt * (kTileM / 128);
+    return t;
+  }
+};
 
 // 32 fp32 values (one block) of a row to 16 bytes of codes; returns the scale byte.
 __device__ __forceinline__ uint32_t quantise_block(float (&h)[32], uint4& codes) {
@@ -297,9 +345,6 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ __align__(8) uint64_t peer_full[kUnitSlots], peer_empty[kUnitSlots];
   __shared__ MxTile peer_ring[kUnitSlots];
   __shared__ uint32_t tmem_base_s;
-  __shared__ int seg_s[kMaxE + 1];
-  __shared__ int cnt_s[kMaxE];
-  __shared__ int tile_start_s[kMaxE + 1];
   __shared__ volatile int abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -337,7 +382,11 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   tc_fence_before();
   cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
   tc_fence_after();
-  pdl_begin();
+  // The down projection follows the up projection, whose blocks all started
+  // after the kernel before it was complete: its row segments can be read now,
+  // and weights loaded, before the up projection is done.
+  const bool early = args.early != 0;
+  if (!early) pdl_begin();
   // All 512 columns are this CTA's, so they start at 0: addresses below are
   // constants (a loaded base would go through registers at every instruction).
   if (tmem_base_s != 0 && threadIdx.x == 0) {
@@ -376,65 +425,69 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   };
 
   if (warp == 10) {
-    int total = 0;
-    if (rank == 0) {
-      // the list of tiles: row segments, and each expert's first tile
-      for (int i = lane; i <= args.E; i += 32) {
-        seg_s[i] = __ldg(args.seg + i);
-        if (i < args.E)
-          cnt_s[i] = args.kept != nullptr ? __ldg(args.kept + i) : __ldg(args.seg + i + 1) - __ldg(args.seg + i);
+    TileList list;
+    list.build(args, args.N / C::OUT_N, lane);
+    const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
+    const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
+    const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
+    // Pair p starts with tile p, which both of its CTAs know; the counter hands
+    // out the tiles from W on.
+    int u = static_cast<int>(blockIdx.x >> 1);
+    int slot = 0, pslot = 0;
+    uint32_t phase = 0, pphase = 0;
+    for (bool first = true;; first = false) {
+      MxTile t{};
+      // a slot is free here once every role of this CTA has read it
+      bool ok = warp_wait(&unit_empty[slot], phase ^ 1u);
+      if (first || rank == 0) {
+        if (ok && !abort_s && u < list.total) t = list.tile(u, C::OUT_N, lane);
+      } else if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&peer_full[pslot], pphase));
+        if (ok) t = *const_cast<const MxTile*>(&peer_ring[pslot]);
+        else give_up();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive_cluster(pempty0 + pslot * 8u);
+        if (++pslot == kUnitSlots) { pslot = 0; pphase ^= 1u; }
       }
-      __syncwarp();
-      build_schedule<kTileM>(args, args.N / C::OUT_N, seg_s, cnt_s, tile_start_s, lane);
-      __syncwarp();
-      total = tile_start_s[args.E];
-    }
-    if (lane == 0) {
-      const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
-      const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
-      const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
-      int slot = 0;
-      uint32_t phase = 0;
-      for (;;) {
-        MxTile t{};
-        // a slot is free here once every role of this CTA has read it; the odd
-        // CTA frees its copy once it has taken it over
-        bool ok = mbar_wait_bounded(&unit_empty[slot], phase ^ 1u);
-        if (rank == 0) {
-          ok = ok && mbar_wait_cluster_bounded(&peer_empty[slot], phase ^ 1u);
-          if (ok && !abort_s) {
-            const int u = static_cast<int>(min(atomicAdd(&args.ctl->gemm_next, 1u), static_cast<unsigned>(total)));
-            if (u < total) t = decode_tile(u, tile_start_s, seg_s, cnt_s, args.E, C::OUT_N);
-          }
-          if (ok) {
-            const uint32_t dst = pring1 + slot * static_cast<uint32_t>(sizeof(MxTile));
+      const bool end = !__all_sync(0xffffffffu, ok && !abort_s && t.rows > 0);
+      if (end) t.rows = 0;
+      if (lane == 0) {
+        unit_ring[slot] = t;
+        mbar_arrive(&unit_full[slot]);
+      }
+      if (rank == 0) {
+        if (!first) {
+          // hand it over; the odd CTA frees the slot once it has taken it
+          ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&peer_empty[pslot], pphase ^ 1u));
+          if (!ok) {
+            give_up();
+          } else if (lane == 0) {
+            const uint32_t dst = pring1 + pslot * static_cast<uint32_t>(sizeof(MxTile));
             st_shared_cluster_u32(dst, static_cast<uint32_t>(t.row0));
             st_shared_cluster_u32(dst + 4, static_cast<uint32_t>(t.rows));
             st_shared_cluster_u32(dst + 8, static_cast<uint32_t>(t.n0));
             st_shared_cluster_u32(dst + 12, static_cast<uint32_t>(t.group));
             st_shared_cluster_u32(dst + 16, static_cast<uint32_t>(t.e));
-            mbar_arrive_cluster(pfull1 + slot * 8u);
+            mbar_arrive_cluster(pfull1 + pslot * 8u);
           }
-        } else {
-          ok = ok && mbar_wait_cluster_bounded(&peer_full[slot], phase);
-          if (ok) {
-            t = *const_cast<const MxTile*>(&peer_ring[slot]);
-            mbar_arrive_cluster(pempty0 + slot * 8u);
-          }
+          if (++pslot == kUnitSlots) { pslot = 0; pphase ^= 1u; }
+        } else if (early) {
+          pdl_begin();  // the counter is the previous kernel's until it is done
         }
-        if (!ok) give_up();
-        if (!ok || abort_s) t.rows = 0;
-        unit_ring[slot] = t;
-        mbar_arrive(&unit_full[slot]);
-        if (++slot == kUnitSlots) { slot = 0; phase ^= 1u; }
-        if (t.rows == 0) break;
+        if (!end) {
+          int v = 0;
+          if (lane == 0) v = static_cast<int>(min(atomicAdd(&args.ctl->gemm_next, 1u), static_cast<unsigned>(list.total)));
+          u = W + __shfl_sync(0xffffffffu, v, 0);
+        }
       }
-      // The last pair to finish resets the tile counter for the next launch
-      // (every pair's last take precedes its increment here).
-      if (rank == 0 && atomicAdd(&args.ctl->gemm_done, 1u) == static_cast<unsigned>(W) - 1u) {
-        atomicExch(&args.ctl->gemm_next, 0u);
-        atomicExch(&args.ctl->gemm_done, 0u);
-      }
+      if (++slot == kUnitSlots) { slot = 0; phase ^= 1u; }
+      if (end) break;
+    }
+    // The last pair to finish resets the tile counter for the next launch
+    // (every pair's last take precedes its increment here).
+    if (rank == 0 && lane == 0 && atomicAdd(&args.ctl->gemm_done, 1u) == static_cast<unsigned>(W) - 1u) {
+      atomicExch(&args.ctl->gemm_next, 0u);
+      atomicExch(&args.ctl->gemm_done, 0u);
     }
   } else if (warp == 0) {
     int stage = 0;
@@ -446,37 +499,54 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const int ngroups = args.N / 128;
     MxTile t;
     bool ok = true;
-    while (ok && next_unit(uslot, uphase, t)) {
+    // early: the first tile's weights go out before the wait for the previous
+    // kernel (stages of a fresh ring are free), its rows after it
+    int ahead = 0;
+    for (bool first = early; ok; first = false) {
+      if (!next_unit(uslot, uphase, t)) break;
       const int arow = t.row0 + 128 * static_cast<int>(rank);
       const int ga = (t.group + static_cast<int>(rank)) * katoms;
       const int gb = (t.e * ngroups + t.n0 / 128) * katoms;
       // SwiGLU: CTA r loads matrix r's columns; otherwise CTA r its half
       const CUtensorMap* mb = EPI == EPI_SWIGLU && rank == 1 ? &tmB1 : &tmB0;
       const int brow = t.e * args.N + t.n0 + (EPI == EPI_SWIGLU ? 0 : C::B_ROWS * static_cast<int>(rank));
+      auto load_weights = [&](int st, int kb) {
+        uint8_t* sa = smem + st * C::STAGE_BYTES;
+        uint8_t* ss = sa + C::OPERANDS;
+        const uint32_t fb = full0 + st * 8u;
+        if (rank == 0) mbar_arrive_expect_tx(&full_bar[st], 2u * C::STAGE_BYTES);
+        tma_load_2d_pair(sa + kBoxBytes, mb, fb, kb * 128, brow);
+        // two scale tiles each (the second is not used where K ends after one)
+        tma_load_2d_pair(ss + 2 * kScaleTile, &tmSB0, fb, 0, gb + 2 * kb);
+        if (C::NB == 2)
+          tma_load_2d_pair(ss + 4 * kScaleTile, EPI == EPI_SWIGLU ? &tmSB1 : &tmSB0, fb, 0,
+                           (EPI == EPI_SWIGLU ? gb : gb + katoms) + 2 * kb);
+      };
+      if (first) {
+        ahead = min(STAGES, nkb);
+        if (elect_one())
+          for (int kb = 0; kb < ahead; ++kb) load_weights(kb, kb);
+        __syncwarp();
+        pdl_begin();
+      }
       for (int kb = 0; kb < nkb; ++kb) {
         if (!warp_wait(&empty_bar[stage], phase ^ 1u)) {
           ok = false;
           break;
         }
         uint8_t* sa = smem + stage * C::STAGE_BYTES;
-        uint8_t* ss = sa + C::OPERANDS;
         const uint32_t fb = full0 + stage * 8u;
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2u * C::STAGE_BYTES);
+          if (kb >= ahead) load_weights(stage, kb);
           tma_load_2d_pair(sa, &tmA, fb, kb * 128, arow);
-          tma_load_2d_pair(sa + kBoxBytes, mb, fb, kb * 128, brow);
-          // two scale tiles each (the second is not used where K ends after one)
-          tma_load_2d_pair(ss, &tmSA, fb, 0, ga + 2 * kb);
-          tma_load_2d_pair(ss + 2 * kScaleTile, &tmSB0, fb, 0, gb + 2 * kb);
-          if (C::NB == 2)
-            tma_load_2d_pair(ss + 4 * kScaleTile, EPI == EPI_SWIGLU ? &tmSB1 : &tmSB0, fb, 0,
-                             (EPI == EPI_SWIGLU ? gb : gb + katoms) + 2 * kb);
+          tma_load_2d_pair(sa + C::OPERANDS, &tmSA, fb, 0, ga + 2 * kb);
         }
         __syncwarp();
         issued_mask |= 1u << stage;
         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
+      ahead = 0;
     }
     // Every load issued must have been consumed by the MMAs (so it landed)
     // before this CTA may leave: the MMA commit of each stage's last load
@@ -485,6 +555,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       if (issued_mask & (1u << s))
         if (!mbar_wait_bounded(&empty_bar[s], (last_parity >> s) & 1u)) set_error(args.ctl, MOE_DEVERR_TIMEOUT);
   } else if (warp == 1) {
+    if (early) pdl_begin();
     if (rank == 0) {
       constexpr uint32_t kIdesc0 = make_idesc_mxf4(256, NMMA, 0);
       constexpr uint32_t kIdesc2 = make_idesc_mxf4(256, NMMA, 2);
@@ -554,6 +625,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     // epilogue warps 2..9: tensor-memory lane quarter = warp % 4 of this CTA's
     // 128 rows, first or second half of the column groups
     constexpr int G = C::OUT_N / 64;  // groups of 32 columns per warp
+    if (early) pdl_begin();
     const int q = warp & 3, half = (warp - 2) >> 2;
     int uslot = 0;
     uint32_t uphase = 0;
@@ -659,6 +731,7 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
     err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, s);
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
+  a.early = 1;
   a.out = static_cast<__nv_bfloat16*>(y);
   a.K = F;
   a.N = d;
