@@ -643,7 +643,7 @@ moe_status_t moe_mxfp4_dequantize_rows(const void* codes, const void* scales, co
 
 size_t moe_expert_ffn_mxfp4_workspace_size(int64_t rows_max, int d, int F, int E) {
   if (rows_max < 0 || d < 1 || F < 1 || E < 1) return 0;
-  return align_up(sizeof(Control));
+  return align_up(sizeof(Control)) + (rows_max <= kMxStreamRows ? mxfp4_stream_partials_bytes() : 0);
 }
 
 moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_scales, const void* w1,
@@ -680,6 +680,7 @@ moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_scales, con
   };
   return from_cuda(launch_ffn_mxfp4(x, weights(w1, w1_scales), weights(w3, w3_scales), weights(w2, w2_scales),
                                     act, rows_max, d, F, E, seg_offsets, nullptr, h, y_perm,
+                                    reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(sizeof(Control))),
                                     static_cast<Control*>(ws), reinterpret_cast<cudaStream_t>(stream), nullptr));
 }
 

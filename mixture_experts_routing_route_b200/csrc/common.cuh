@@ -19,7 +19,9 @@ struct Control {
   uint32_t wait_limit_us; // limit of the waits between CTAs; 0: 2 s
   uint32_t gemm_next;     // CTA-pair GEMM: next work unit (reset by the last pair)
   uint32_t gemm_done;     // CTA-pair GEMM: pairs that finished (reset by the last pair)
-  uint32_t reserved[57];
+  uint32_t stream_ticket[40];  // MXFP4 decode GEMM: pieces of a cut tile that arrived, a byte
+                               // per block (reset by the last one)
+  uint32_t reserved[17];
 };
 static_assert(sizeof(Control) == 256, "control block is 256 bytes");
 
@@ -355,6 +357,16 @@ cudaError_t launch_gather_backward(const void* dx_perm, const int32_t* slot_to_r
                                    const void* dx_in, size_t elem, int T, int d, int k,
                                    int64_t rows_max, void* dx, Control* ctl, cudaStream_t s);
 
+// Decode-size MXFP4 GEMM (gemm_mxfp4_stream.cu): its most rows, and its most
+// blocks (the bytes of Control::stream_ticket).
+constexpr int kMxStreamRows = 32;
+constexpr int kMxStreamBlocks = 160;
+int stream_blocks();
+// Its partial sums: two pieces per block of two matrices x 32 tokens x 128.
+inline size_t mxfp4_stream_partials_bytes() {
+  return static_cast<size_t>(kMxStreamBlocks) * 2 * 2 * kMxStreamRows * 128 * sizeof(float);
+}
+
 // MXFP4 (see mxfp4.cuh). Rows sorted by expert and expert weights [E, N, K].
 struct MxRows {
   uint8_t* codes;   // [rows_max, K / 2]
@@ -375,11 +387,13 @@ cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* sc
                                          int E, int64_t rows_max, int K, moe_dtype_t dt, void* out,
                                          Control* ctl, cudaStream_t s);
 // The experts' FFN on MXFP4 rows and weights; y bf16. kept: rows of each
-// expert (binned layout), NULL: seg[e + 1] - seg[e].
+// expert (binned layout), NULL: seg[e + 1] - seg[e]. partials:
+// mxfp4_stream_partials_bytes() when rows_max <= kMxStreamRows. early_up: seg,
+// kept and the weights were complete before the last kernel on s began.
 cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
                              moe_act_t act, int64_t rows_max, int d, int F, int E, const int32_t* seg,
-                             const int32_t* kept, const MxRows& h, void* y, Control* ctl, cudaStream_t s,
-                             cudaEvent_t after_up);
+                             const int32_t* kept, const MxRows& h, void* y, float* partials, Control* ctl,
+                             cudaStream_t s, cudaEvent_t after_up, bool early_up = false);
 
 // Expert-parallel dispatch plans (ep.cu). Experts are owned in contiguous
 // blocks of e_loc per rank.

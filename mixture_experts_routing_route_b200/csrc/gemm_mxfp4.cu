@@ -43,119 +43,17 @@
 // cluster scope) off every other role's path, and takes no tile so early that
 // a slow pair would hold work an idle one could do.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
-#include "gemm_common.cuh"
-#include "mxfp4.cuh"
-#include "ptx.cuh"
-#include <cudaTypedefs.h>
+#include "mxfp4_gemm.cuh"
 
 namespace moe {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 namespace {
 
 constexpr int kTileM = 256;
-constexpr int kBoxBytes = 128 * 128;  // 128 rows x 128 bytes (256 values of K)
 constexpr int kEpiWarps = 8;               // per CTA
 constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr int kUnitSlots = 3;              // ring of tiles published to a CTA's roles
 constexpr uint32_t kUnitReaders = 1 + kEpiWarps;  // producer, epilogue warps (and the even CTA's MMA warp)
-
-enum { EPI_SWIGLU = 0, EPI_GELU = 1, EPI_STORE = 2 };
-
-// Hardware exponential (base 2) and reciprocal, subnormals flushed: one
-// instruction each, within a few ulp.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The up projection's activations. Their result is rounded to E2M1, so a few
-// ulp never show; a tile has up to 32768 of them, and they bound the kernel
-// where K is short (with erff the epilogue of a 128 x 256 tile took 11500
-// cycles, the MMAs of K = 1024 2400).
-//
-// silu(g) = g / (1 + e^-g): for g < -128 ln 2 the exponential is Inf, its
-// reciprocal 0 and the result -0, the limit.
-__device__ __forceinline__ float silu_fast(float g) { return g * rcp(1.0f + ex2(-1.44269504f * g)); }
-
-// gelu(z) = z Phi(z) = max(z, 0) - |z| Phi(-|z|), Phi(-a) = erfc(a / sqrt 2) / 2
-// by Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26:
-// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2), t = 1 / (1 + p x), within 1.5e-7
-// (here the five coefficients are halved and p is divided by sqrt 2).
-__device__ __forceinline__ float gelu_fast(float z) {
-  const float a = fabsf(z);
-  const float t = rcp(fmaf(0.23164190f, a, 1.0f));
-  const float e = ex2(-0.72134752f * z * z);  // e^(-z^2 / 2)
-  float p = fmaf(0.5307027145f, t, -0.7265760135f);
-  p = fmaf(p, t, 0.7107068705f);
-  p = fmaf(p, t, -0.142248368f);
-  p = fmaf(p, t, 0.127414796f);
-  return fmaxf(z, 0.0f) - a * (p * t) * e;
-}
-
-struct MxArgs {
-  const int32_t* seg;    // [E+1] row segment offsets
-  const int32_t* kept;   // [E] rows of each expert from seg[e] (binned layout), or null
-  uint8_t* out_codes;    // up projection: h codes [rows_max, N/2]
-  uint8_t* out_scales;   // up projection: h scales
-  __nv_bfloat16* out;    // down projection: [rows_max, N]
-  int E;
-  int K;
-  int N;  // output columns
-  int early;  // seg, kept and the weights were complete before the previous kernel on the stream began
-  long long rows_max;
-  Control* ctl;
-};
-
-// ------------------------------------------------------------ tcgen05, mxf4
-// Instruction descriptor of kind::mxf4: E2M1 operands (1 at bits 7 and 10),
-// both K-major, N / 8 at bit 17, scales UE8M0 (bit 23), M / 128 at bit 27; the
-// ids of the scale bytes to use (0 or 2) go to bits 4 (B) and 29 (A).
-__host__ __device__ constexpr uint32_t make_idesc_mxf4(int M, int N, uint32_t sf_id) {
-  return (sf_id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
-         (static_cast<uint32_t>(M >> 7) << 27) | (sf_id << 29);
-}
-
-// True in one thread of a converged warp, the same one every time. The tensor
-// core's and TMA's instructions take warp-uniform operands: issued under this
-// predicate from code that the whole warp runs they cost a few cycles each,
-// from a branch that one lane took (lane == 0) about 80 (measured: a stage's
-// eleven took 885 cycles, more than the MMAs themselves).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-  return ok != 0;
-}
-
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
-
-// Descriptor of scale tiles at a shared-memory address: no swizzle, 32 rows of
-// 16 bytes, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t make_scale_desc(uint32_t smem_addr) {
-  return static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128 >> 4) << 32) |
-         (static_cast<uint64_t>(1u) << 46);
-}
-
-// One 512-byte scale tile of each CTA of the pair to 4 columns of its tensor memory, replicated to the
-// four 32-lane quarters.
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
 
 // Arrive on another CTA's mbarrier without a release: for arrivals that order
 // tensor-memory loads only (complete, and fenced by tcgen05.fence).
@@ -176,80 +74,6 @@ struct Cfg {
   static constexpr int SF_COL = 480;
   static constexpr int TMEM_COLS = 512;
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + 1024;
-};
-
-struct __align__(16) MxTile {
-  int row0, rows, n0;
-  int group;  // row group (of 128) of its first row's scales
-  int e;
-  int pad[3];
-};
-
-// The list of tiles, held by one warp: lane l has experts [8 l, 8 l + 8) with
-// their first rows, row counts and first tiles. Tiles are ordered
-// expert-major, then N tile, M tile fastest.
-struct TileList {
-  int seg[8], cnt[8], start[8];
-  int total;
-
-  __device__ __forceinline__ void build(const MxArgs& args, int ntn, int lane) {
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = lane * 8 + i;
-      seg[i] = cnt[i] = 0;
-      int end = 0;
-      if (e < args.E) {
-        seg[i] = __ldg(args.seg + e);
-        end = __ldg(args.seg + e + 1);
-        cnt[i] = args.kept != nullptr ? __ldg(args.kept + e) : end - seg[i];
-      }
-      // rows out of range are reported and their expert gets no tiles
-      if (cnt[i] < 0 || seg[i] < 0 || static_cast<long long>(seg[i]) + cnt[i] > min(args.rows_max, static_cast<long long>(end))) {
-        set_error(args.ctl, MOE_DEVERR_ROW_RANGE);
-        cnt[i] = 0;
-      }
-      start[i] = ((cnt[i] + kTileM - 1) / kTileM) * ntn;
-      sum += start[i];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += n;
-    }
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    int run = incl - sum;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = start[i];
-      start[i] = run;
-      run += n;
-    }
-  }
-
-  // Tile u < total, by the whole warp.
-  __device__ __forceinline__ MxTile tile(int u, int out_n, int lane) const {
-    int s = -1, c = 0, st = 0, e = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (start[i] <= u) { s = seg[i]; c = cnt[i]; st = start[i]; e = lane * 8 + i; }
-    // the last lane with an expert that starts at or before u
-    const int src = 31 - __clz(__ballot_sync(0xffffffffu, s >= 0));
-    s = __shfl_sync(0xffffffffu, s, src);
-    c = __shfl_sync(0xffffffffu, c, src);
-    st = __shfl_sync(0xffffffffu, st, src);
-    MxTile t;
-    t.e = __shfl_sync(0xffffffffu, e, src);
-    const int mt_e = (c + kTileM - 1) / kTileM;
-    const int local = u - st;
-    const int nt = local / mt_e, mt = local - nt * mt_e;
-    t.row0 = s + mt * kTileM;
-    t.rows = min(kTileM, c - mt * kTileM);
-    t.n0 = nt * out_n;
-    t.group = s / 128 + t.e + mt * (kTileM / 128);
-    return t;
-  }
 };
 
 // 32 fp32 values (one block) of a row to 16 bytes of codes; returns the scale byte.
@@ -425,7 +249,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   };
 
   if (warp == 10) {
-    TileList list;
+    TileList<kTileM> list;
     list.build(args, args.N / C::OUT_N, lane);
     const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
     const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
@@ -588,14 +412,14 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 if (at < atoms) {
                   const uint32_t sfa = tmem_base + C::SF_COL + (set ^ at) * 16;
                   const uint32_t sfb = sfa + 4;
-                  copy_scales(sfa, sdesc0 + so + at * (kScaleTile >> 4));
+                  copy_scales<2>(sfa, sdesc0 + so + at * (kScaleTile >> 4));
 #pragma unroll
                   for (int j = 0; j < C::NB; ++j)
-                    copy_scales(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
+                    copy_scales<2>(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
 #pragma unroll
                   for (int kk = 0; kk < 2; ++kk) {
                     const uint32_t off = so + (at * 2 + kk) * 2;
-                    umma_mxf4(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
+                    umma_mxf4<2>(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
                               (kb | at | kk) != 0 ? 1u : 0u);
                   }
                 }
@@ -655,34 +479,6 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   }
 }
 
-// Codes [rows, cols / 2 bytes], box 128 bytes x box_rows, 128-byte swizzle.
-bool make_tma_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {row_bytes, rows};
-  cuuint64_t strides[1] = {row_bytes};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// Scale tiles [tiles, 512 bytes], box two tiles.
-bool make_tma_scales(CUtensorMap* m, const void* base, uint64_t tiles) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {kScaleTile / 4, tiles};
-  cuuint64_t strides[1] = {kScaleTile};
-  cuuint32_t box[2] = {kScaleTile / 4, 2};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 template <int EPI, int NMMA>
 cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
   using C = Cfg<EPI, NMMA>;
@@ -706,8 +502,8 @@ cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, 
 
 cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
                              moe_act_t act, int64_t rows_max, int d, int F, int E, const int32_t* seg,
-                             const int32_t* kept, const MxRows& h, void* y, Control* ctl, cudaStream_t s,
-                             cudaEvent_t after_up) {
+                             const int32_t* kept, const MxRows& h, void* y, float* partials, Control* ctl,
+                             cudaStream_t s, cudaEvent_t after_up, bool early_up) {
   if (rows_max <= 0) {
     if (after_up) cudaEventRecord(after_up, s);
     return cudaSuccess;
@@ -722,8 +518,15 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.out_scales = h.scales;
   a.K = d;
   a.N = F;
+  a.early = early_up ? 1 : 0;
+  // A decode step's rows (32 at most, so no expert has more) go through the
+  // weight stream: one token of a Mixtral-shaped layer takes 47 us there,
+  // 57 us here.
+  const bool stream = rows_max <= kMxStreamRows;
   cudaError_t err;
-  if (act == MOE_ACT_SWIGLU)
+  if (stream)
+    err = launch_stream_mxfp4_up(x, w1, w3, act, a, partials, s);
+  else if (act == MOE_ACT_SWIGLU)
     err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
   else if (F % 256 == 0)
     err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
@@ -735,6 +538,7 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.out = static_cast<__nv_bfloat16*>(y);
   a.K = F;
   a.N = d;
+  if (stream) return launch_stream_mxfp4_down(h, w2, a, partials, s);
   if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
   return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
 }

@@ -57,6 +57,17 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   return r;
 }
 
+// One scaled value to its code.
+__device__ __forceinline__ uint32_t e2m1(float v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b, z;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 z, %2, %2;\n\t"
+      "mov.b32 %0, {b, z, z, z};\n\t}"
+      : "=r"(r) : "f"(v), "f"(0.0f));
+  return r;
+}
+
 // Value of one code (0..15) at scale 1.
 __device__ __forceinline__ float e2m1_value(uint32_t c) {
   const uint32_t m = c & 7u;

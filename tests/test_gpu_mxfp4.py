@@ -253,7 +253,20 @@ FFN = [
 ]
 
 
-@pytest.mark.parametrize("E,d,F,counts,act", FFN)
+# a decode step: at most 32 rows in all (the weight stream, tiles cut between blocks)
+FEW = [
+    (1, 128, 128, [1], "swiglu"),
+    (8, 4096, 1792, [0, 1, 0, 0, 0, 0, 1, 0], "swiglu"),
+    (4, 384, 640, [3, 0, 8, 1], "gelu"),          # half stages
+    (2, 2176, 3200, [31, 1], "swiglu"),
+    (256, 256, 384, [1 if e % 9 == 4 else 0 for e in range(256)], "gelu"),
+    (3, 128, 4096, [0, 32, 0], "swiglu"),          # one stage a tile up, sixteen down
+    (6, 7168, 128, [5, 0, 0, 2, 0, 25], "swiglu"),  # a tile cut between many blocks
+    (64, 512, 2048, [1 if e in (0, 17, 40, 63) else 0 for e in range(64)], "gelu"),
+]
+
+
+@pytest.mark.parametrize("E,d,F,counts,act", FFN + FEW)
 @pytest.mark.parametrize("extra", [0, 19])
 def test_ffn(E, d, F, counts, act, extra):
     ex = Experts(E, d, F, act, seed=d + F)
@@ -281,9 +294,10 @@ def test_ffn_nan_rows_stay_alone():
     assert bad.sum().item() == 1 and bad[45].item() and torch.isnan(y[45]).all()
 
 
-def test_ffn_repeats_bit_for_bit_on_one_workspace_and_in_a_graph():
+@pytest.mark.parametrize("counts", [[130, 0, 4, 260, 1, 70], [3, 0, 4, 0, 1, 17]])
+def test_ffn_repeats_bit_for_bit_on_one_workspace_and_in_a_graph(counts):
     ex = Experts(6, 512, 1024, "swiglu", 4)
-    rows, seg, xc, xs = rows_of(ex, [130, 0, 4, 260, 1, 70], 3, 5)
+    rows, seg, xc, xs = rows_of(ex, counts, 3, 5)
     hc, hs, y, ws = run_ffn(ex, xc, xs, rows, seg)
     for _ in range(3):
         a, b, c, _ = run_ffn(ex, xc, xs, rows, seg, ws=ws)
@@ -299,6 +313,21 @@ def test_ffn_repeats_bit_for_bit_on_one_workspace_and_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(got[0], hc) and torch.equal(got[2], y)
     assert abi.moe_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("counts", [[40, 0, 24], [1, 0, 6]])
+def test_ffn_of_one_row_does_not_depend_on_the_others(counts):
+    """The same rows alone (few: the weight stream) and among others give the
+    same h, and y within the two orders of summation."""
+    ex = Experts(3, 1024, 768, "swiglu", 9)
+    rows, seg, xc, xs = rows_of(ex, counts, 0, 10)
+    hc, hs, y, _ = run_ffn(ex, xc, xs, rows, seg)
+    solo = torch.tensor([0, 1, 1, 1], dtype=torch.int32, device=DEV)
+    hc1, hs1, y1, ws = run_ffn(ex, xc[:1].contiguous(), xs, 1, solo)
+    assert abi.moe_get_device_error(ws) == 0
+    same = (hc1[:ex.F // 2] == hc[:ex.F // 2]).float().mean().item()
+    assert same >= 0.99  # a sum next to a rounding step may fall on its other side
+    assert float((y1[0].double() - y[0].double()).norm() / y[0].double().norm()) <= 2.0 ** -6
 
 
 def test_ffn_bad_segments_set_the_error_bit():
