@@ -50,6 +50,23 @@ __device__ __forceinline__ int stage_owner(long long s, long long stages, int W)
   return static_cast<int>(((s + 1) * W - 1) / stages);
 }
 
+// Eight token columns from c on of each matrix's accumulator.
+template <int MATS>
+__device__ __forceinline__ void load_columns(uint32_t tbase, int c, float (&v)[MATS][8]) {
+  uint32_t r[MATS][8];
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[m][0]), "=r"(r[m][1]), "=r"(r[m][2]), "=r"(r[m][3]), "=r"(r[m][4]), "=r"(r[m][5]),
+                   "=r"(r[m][6]), "=r"(r[m][7])
+                 : "r"(tbase + m * kTok + c));
+  tmem_ld_wait();
+#pragma unroll
+  for (int m = 0; m < MATS; ++m)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[m][k] = __uint_as_float(r[m][k]);
+}
+
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 template <int EPI>
@@ -64,7 +81,7 @@ stream_mxf4(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CU
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2], tfree_bar[2], drain_bar;
   __shared__ uint32_t tmem_base_s;
-  __shared__ int last_s, ok_s[2];
+  __shared__ int late_s, flag_s[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -230,107 +247,118 @@ stream_mxf4(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CU
     if (early) pdl_begin();
     const int q = warp & 3;  // tensor-memory lane quarter
     const int col = q * 32 + lane;  // output column in the tile
-    bool ok;
+    const bool lead = threadIdx.x == kThreads - kEpiThreads;
     int i = 0;
     for (int s = beg; s < end; ++i) {
       const int u = s / nkb;
       const int s_end = min(end, (u + 1) * nkb);
       const MxTile t = list.tile(u, 128, lane);
-      // one thread decides for the four warps, which share a barrier below and
-      // so have to leave together
-      if (threadIdx.x == kThreads - kEpiThreads) ok_s[i & 1] = mbar_wait_bounded(&tfull_bar[i & 1], (i >> 1) & 1);
+      // A tile cut between blocks c0..c1: whoever comes last adds the pieces, in
+      // the order of K, the others leave theirs in the workspace. Usually that
+      // is the block where the tile begins, at the end of its stages: the next
+      // one had its piece first. So look before the wait for the MMAs whether
+      // the other pieces are there; then this one need not go through memory.
+      const long long s0 = static_cast<long long>(u) * nkb;
+      const int c0 = stage_owner(s0, stages, W), c1 = stage_owner(s0 + nkb - 1, stages, W);
+      const uint32_t others = static_cast<uint32_t>(c1 - c0);
+      auto piece = [&](int c) -> float* {  // block c's: 0 for a tile begun before its stages, else 1
+        return partials + (static_cast<size_t>(c) * 2 + (stage_begin(c, stages, W) > s0 ? 0 : 1)) * (MATS * kTok * 128) + col;
+      };
+      // tickets: a byte per block in which a cut tile begins
+      uint32_t* word = &args.ctl->stream_ticket[c0 >> 2];
+      const int sh = 8 * (c0 & 3);
+      // one thread decides for the four warps, which share barriers and so have
+      // to leave together
+      if (lead) {
+        bool last = true;
+        if (others > 0) {
+          last = ((*reinterpret_cast<volatile uint32_t*>(word) >> sh) & 255u) == others;
+          if (last) atomicSub(word, others << sh);
+          __threadfence();
+        }
+        const bool ok = mbar_wait_bounded(&tfull_bar[i & 1], (i >> 1) & 1);
+        flag_s[i & 1] = (ok ? 1 : 0) | (last ? 2 : 0);
+      }
       epi_barrier();
-      ok = ok_s[i & 1] != 0;
-      if (!ok) {
+      const int flag = flag_s[i & 1];
+      if ((flag & 1) == 0) {
         set_error(args.ctl, MOE_DEVERR_TIMEOUT);
         break;
       }
       (void)mbar_try_wait(&tfull_bar[i & 1], (i >> 1) & 1);  // complete: each thread observes it
       tc_fence_after();
-      float v[MATS][kTok];
-      {
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (i & 1) * (MATS * kTok);
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (i & 1) * (MATS * kTok);
+      bool finish = (flag & 2) != 0;
+      if (!finish) {
+        float* mine = piece(me);
+#pragma unroll 1
+        for (int c = 0; c < t.rows; c += 8) {
+          float v[MATS][8];
+          load_columns(tb, c, v);
 #pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tb + m * kTok, r);
-          tmem_ld_wait();
+          for (int m = 0; m < MATS; ++m)
 #pragma unroll
-          for (int c = 0; c < kTok; ++c) v[m][c] = __uint_as_float(r[c]);
+            for (int k = 0; k < 8; ++k)
+              if (c + k < t.rows) __stcg(mine + (m * kTok + c + k) * 128, v[m][k]);
+        }
+        __threadfence();
+        epi_barrier();
+        if (lead) {
+          const uint32_t before = (atomicAdd(word, 1u << sh) >> sh) & 255u;
+          if (before == others) atomicSub(word, (others + 1u) << sh);
+          late_s = before == others;
+          __threadfence();
+        }
+        epi_barrier();
+        finish = late_s != 0;
+      }
+      if (finish) {
+#pragma unroll 1
+        for (int c = 0; c < t.rows; c += 8) {
+          float v[MATS][8];
+          load_columns(tb, c, v);
+          if (others > 0) {
+            float own[MATS][8];
+#pragma unroll
+            for (int m = 0; m < MATS; ++m)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) { own[m][k] = v[m][k]; v[m][k] = 0.f; }
+#pragma unroll 1
+            for (int b = c0; b <= c1; ++b) {
+              const float* p = piece(b);
+#pragma unroll
+              for (int m = 0; m < MATS; ++m)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  v[m][k] += b == me ? own[m][k] : c + k < t.rows ? __ldcg(p + (m * kTok + c + k) * 128) : 0.f;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (c + k >= t.rows) break;
+            const size_t row = static_cast<size_t>(t.row0) + c + k;
+            if constexpr (EPI == EPI_STORE) {
+              args.out[row * args.N + t.n0 + col] = __float2bfloat16_rn(v[0][k]);
+            } else {
+              const float h = EPI == EPI_SWIGLU ? silu_fast(v[0][k]) * v[MATS - 1][k] : gelu_fast(v[0][k]);
+              const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+              const uint32_t sb = mx_scale_byte(top);
+              // eight lanes' codes to one word
+              uint32_t w = sb == 255u ? 0u : e2m1(h * mx_inv_scale(sb)) << (4 * (lane & 7));
+              w |= __shfl_xor_sync(0xffffffffu, w, 1);
+              w |= __shfl_xor_sync(0xffffffffu, w, 2);
+              w |= __shfl_xor_sync(0xffffffffu, w, 4);
+              if ((lane & 7) == 0)
+                *reinterpret_cast<uint32_t*>(args.out_codes + row * (args.N / 2) + (t.n0 + col) / 2) = w;
+              if (lane == 0)
+                args.out_scales[mx_scale_at(t.group, args.N / 128, c + k, t.n0 / 32 + q)] = static_cast<uint8_t>(sb);
+            }
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tfree_bar[i & 1]);
-
-      bool finish = true;
-      if (s != u * nkb || s_end != (u + 1) * nkb) {
-        // A piece of a tile: leave it in the workspace; the last of the tile's
-        // blocks adds them all, in the order of K.
-        const long long s0 = static_cast<long long>(u) * nkb;
-        const int c0 = stage_owner(s0, stages, W), c1 = stage_owner(s0 + nkb - 1, stages, W);
-        auto piece = [&](int c) -> float* {  // block c's: 0 for a tile begun before its stages, else 1
-          return partials + (static_cast<size_t>(c) * 2 + (stage_begin(c, stages, W) > s0 ? 0 : 1)) * (MATS * kTok * 128) + col;
-        };
-        float* mine = piece(me);
-#pragma unroll
-        for (int m = 0; m < MATS; ++m)
-#pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (c < t.rows) __stcg(mine + (m * kTok + c) * 128, v[m][c]);
-        __threadfence();
-        epi_barrier();
-        if (threadIdx.x == kThreads - kEpiThreads) {
-          // tickets: a byte per block in which a cut tile begins
-          uint32_t* word = &args.ctl->stream_ticket[c0 >> 2];
-          const int sh = 8 * (c0 & 3);
-          const uint32_t n = static_cast<uint32_t>(c1 - c0 + 1);
-          const uint32_t before = (atomicAdd(word, 1u << sh) >> sh) & 255u;
-          if (before == n - 1u) atomicSub(word, n << sh);
-          last_s = before == n - 1u;
-          __threadfence();
-        }
-        epi_barrier();
-        finish = last_s != 0;
-        if (finish) {
-          __threadfence();
-#pragma unroll
-          for (int m = 0; m < MATS; ++m)
-#pragma unroll
-            for (int c = 0; c < kTok; ++c) v[m][c] = 0.f;
-          for (int b = c0; b <= c1; ++b) {
-            const float* p = piece(b);
-#pragma unroll
-            for (int m = 0; m < MATS; ++m)
-#pragma unroll
-              for (int c = 0; c < kTok; ++c)
-                if (c < t.rows) v[m][c] += __ldcg(p + (m * kTok + c) * 128);
-          }
-        }
-        epi_barrier();  // last_s is read before the next piece sets it
-      }
-      if (finish) {
-#pragma unroll
-        for (int c = 0; c < kTok; ++c) {
-          if (c >= t.rows) break;
-          const size_t row = static_cast<size_t>(t.row0) + c;
-          if constexpr (EPI == EPI_STORE) {
-            args.out[row * args.N + t.n0 + col] = __float2bfloat16_rn(v[0][c]);
-          } else {
-            const float h = EPI == EPI_SWIGLU ? silu_fast(v[0][c]) * v[MATS - 1][c] : gelu_fast(v[0][c]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            const uint32_t sb = mx_scale_byte(top);
-            // eight lanes' codes to one word
-            uint32_t w = sb == 255u ? 0u : e2m1(h * mx_inv_scale(sb)) << (4 * (lane & 7));
-            w |= __shfl_xor_sync(0xffffffffu, w, 1);
-            w |= __shfl_xor_sync(0xffffffffu, w, 2);
-            w |= __shfl_xor_sync(0xffffffffu, w, 4);
-            if ((lane & 7) == 0)
-              *reinterpret_cast<uint32_t*>(args.out_codes + row * (args.N / 2) + (t.n0 + col) / 2) = w;
-            if (lane == 0) args.out_scales[mx_scale_at(t.group, args.N / 128, c, t.n0 / 32 + q)] = static_cast<uint8_t>(sb);
-          }
-        }
-      }
       s = s_end;
     }
   }
