@@ -2,6 +2,7 @@
 // layout, and the stage launches on the caller's stream. Nothing here
 // allocates device memory or synchronises, except moe_get_device_error.
 #include "common.cuh"
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -567,6 +568,15 @@ static moe_status_t check_mxfp4(moe_dtype_t dtype, int E, int K, int N) {
   return MOE_OK;
 }
 
+// The products count rows, scale tiles and stages in 32 bits.
+static moe_status_t check_mxfp4_tiles(int64_t rows_max, int d, int F, int E) {
+  const int64_t kd = d / 128, kf = F / 128;
+  if (kd > 8192 || kf > 8192 || E * kd * kf >= INT_MAX || static_cast<int64_t>(E) * std::max(d, F) >= INT_MAX ||
+      (rows_max / 128 + E) * std::max(kd, kf) >= INT_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 size_t moe_mxfp4_weight_scales_size(int E, int K, int N) {
   if (E < 1 || K < 1 || N < 1) return 0;
   return static_cast<size_t>(E) * ((static_cast<size_t>(N) + 127) / 128) * ((static_cast<size_t>(K) + 127) / 128) * 512;
@@ -654,6 +664,7 @@ moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_scales, con
   MOE_CHECK(check_mxfp4(MOE_BF16, E, d, F));
   if (act != MOE_ACT_GELU && act != MOE_ACT_SWIGLU) return MOE_ERR_INVALID;
   if (rows_max < 0 || rows_max >= INT_MAX) return MOE_ERR_INVALID;
+  MOE_CHECK(check_mxfp4_tiles(rows_max, d, F, E));
   MOE_NEED(w1);
   MOE_NEED(w1_scales);
   MOE_NEED(w2);

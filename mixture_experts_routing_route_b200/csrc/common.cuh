@@ -19,9 +19,12 @@ struct Control {
   uint32_t wait_limit_us; // limit of the waits between CTAs; 0: 2 s
   uint32_t gemm_next;     // CTA-pair GEMM: next work unit (reset by the last pair)
   uint32_t gemm_done;     // CTA-pair GEMM: pairs that finished (reset by the last pair)
-  uint32_t stream_ticket[40];  // MXFP4 decode GEMM: pieces of a cut tile that arrived, a byte
-                               // per block (reset by the last one)
-  uint32_t reserved[17];
+  uint32_t stream_ticket[40];  // MXFP4 decode FFN: pieces of a cut tile that arrived, a byte
+                               // per range (reset by the last one)
+  uint32_t stream_next;     // the same: next range (reset by the last block)
+  uint32_t stream_up_done;  // the same: ranges of the up projection done (reset likewise)
+  uint32_t stream_done;     // the same: blocks that finished (reset likewise)
+  uint32_t reserved[14];
 };
 static_assert(sizeof(Control) == 256, "control block is 256 bytes");
 
@@ -357,11 +360,10 @@ cudaError_t launch_gather_backward(const void* dx_perm, const int32_t* slot_to_r
                                    const void* dx_in, size_t elem, int T, int d, int k,
                                    int64_t rows_max, void* dx, Control* ctl, cudaStream_t s);
 
-// Decode-size MXFP4 GEMM (gemm_mxfp4_stream.cu): its most rows, and its most
+// Decode-size MXFP4 FFN (gemm_mxfp4_stream.cu): its most rows, and its most
 // blocks (the bytes of Control::stream_ticket).
 constexpr int kMxStreamRows = 32;
 constexpr int kMxStreamBlocks = 160;
-int stream_blocks();
 // Its partial sums: two pieces per block of two matrices x 32 tokens x 128.
 inline size_t mxfp4_stream_partials_bytes() {
   return static_cast<size_t>(kMxStreamBlocks) * 2 * 2 * kMxStreamRows * 128 * sizeof(float);

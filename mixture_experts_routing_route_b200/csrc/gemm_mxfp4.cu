@@ -168,6 +168,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   // the even CTA's scheduler to the odd one's: full in the odd, empty in the even CTA
   __shared__ __align__(8) uint64_t peer_full[kUnitSlots], peer_empty[kUnitSlots];
   __shared__ MxTile peer_ring[kUnitSlots];
+  __shared__ Segments segments;
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
 
@@ -250,7 +251,9 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 
   if (warp == 10) {
     TileList<kTileM> list;
-    list.build(args, args.N / C::OUT_N, lane);
+    load_segments(segments, args, lane, 32);
+    __syncwarp();
+    list.build(args, segments, args.N / C::OUT_N, lane);
     const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
     const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
     const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
@@ -512,21 +515,27 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.seg = seg;
   a.kept = kept;
   a.E = E;
+  a.d = d;
+  a.F = F;
   a.rows_max = rows_max;
   a.ctl = ctl;
+  a.early = early_up ? 1 : 0;
   a.out_codes = h.codes;
   a.out_scales = h.scales;
+  a.out = static_cast<__nv_bfloat16*>(y);
+  // A decode step's rows (32 at most, so no expert has more) go through the
+  // weight stream: one token of a Mixtral-shaped layer takes STREAM us there,
+  // 57 us here.
+  if (rows_max <= kMxStreamRows) {
+    a.partials = partials;
+    const cudaError_t err = launch_stream_ffn_mxfp4(x, w1, w3, w2, act, h, a, s);
+    if (after_up) cudaEventRecord(after_up, s);
+    return err;
+  }
   a.K = d;
   a.N = F;
-  a.early = early_up ? 1 : 0;
-  // A decode step's rows (32 at most, so no expert has more) go through the
-  // weight stream: one token of a Mixtral-shaped layer takes 47 us there,
-  // 57 us here.
-  const bool stream = rows_max <= kMxStreamRows;
   cudaError_t err;
-  if (stream)
-    err = launch_stream_mxfp4_up(x, w1, w3, act, a, partials, s);
-  else if (act == MOE_ACT_SWIGLU)
+  if (act == MOE_ACT_SWIGLU)
     err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
   else if (F % 256 == 0)
     err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
@@ -535,10 +544,8 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
   a.early = 1;
-  a.out = static_cast<__nv_bfloat16*>(y);
   a.K = F;
   a.N = d;
-  if (stream) return launch_stream_mxfp4_down(h, w2, a, partials, s);
   if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
   return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
 }

@@ -17,10 +17,12 @@ struct MxArgs {
   uint8_t* out_scales;   // up projection: h scales
   __nv_bfloat16* out;    // down projection: [rows_max, N]
   int E;
-  int K;
-  int N;  // output columns
+  int d, F;  // the layer's
+  int K;     // of one projection: what is summed over
+  int N;     // of one projection: output columns
   int early;  // seg, kept and the weights were complete before the previous kernel on the stream began
   long long rows_max;
+  float* partials;  // decode kernel: mxfp4_stream_partials_bytes()
   Control* ctl;
 };
 
@@ -131,6 +133,21 @@ struct __align__(16) MxTile {
   int pad[3];
 };
 
+// The experts' row segments in shared memory, read once per block: every block
+// wants the same few lines at the same time, and one L2 slice serves them (a
+// read by every lane of every warp that needs them cost 3 us).
+struct Segments {
+  int seg[kMaxE + 1], kept[kMaxE];
+};
+
+// By `threads` threads; the caller orders the writes before the reads.
+__device__ __forceinline__ void load_segments(Segments& s, const MxArgs& args, int thread, int threads) {
+  for (int i = thread; i <= args.E; i += threads) {
+    s.seg[i] = __ldcg(args.seg + i);
+    if (args.kept != nullptr && i < args.E) s.kept[i] = __ldcg(args.kept + i);
+  }
+}
+
 // The list of tiles, held by one warp: lane l has experts [8 l, 8 l + 8) with
 // their first rows, row counts and first tiles. Tiles are ordered
 // expert-major, then N tile, M tile fastest.
@@ -139,26 +156,26 @@ struct TileList {
   int seg[8], cnt[8], start[8];
   int total;
 
-  __device__ __forceinline__ void build(const MxArgs& args, int ntn, int lane) {
+  // From the segment list in shared memory (see load_segments).
+  __device__ __forceinline__ void build(const MxArgs& args, const Segments& in, int ntn, int lane) {
     int sum = 0;
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane * 8 + i;
-      seg[i] = cnt[i] = 0;
-      int end = 0;
-      if (e < args.E) {
-        seg[i] = __ldg(args.seg + e);
-        end = __ldg(args.seg + e + 1);
-        cnt[i] = args.kept != nullptr ? __ldg(args.kept + e) : end - seg[i];
-      }
+      const bool there = e < args.E;
+      seg[i] = there ? in.seg[e] : 0;
+      const int end = there ? in.seg[e + 1] : 0;
+      cnt[i] = !there ? 0 : args.kept != nullptr ? in.kept[e] : end - seg[i];
       // rows out of range are reported and their expert gets no tiles
       if (cnt[i] < 0 || seg[i] < 0 || static_cast<long long>(seg[i]) + cnt[i] > min(args.rows_max, static_cast<long long>(end))) {
-        set_error(args.ctl, MOE_DEVERR_ROW_RANGE);
+        bad = true;
         cnt[i] = 0;
       }
       start[i] = ((cnt[i] + TILE_M - 1) / TILE_M) * ntn;
       sum += start[i];
     }
+    if (bad) set_error(args.ctl, MOE_DEVERR_ROW_RANGE);
     int incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -229,10 +246,8 @@ inline bool make_tma_scales(CUtensorMap* m, const void* base, uint64_t tiles) {
 
 }  // namespace
 
-// The decode-size kernels (gemm_mxfp4_stream.cu).
-cudaError_t launch_stream_mxfp4_up(const MxRows& x, const MxWeights& w1, const MxWeights& w3, moe_act_t act,
-                                   const MxArgs& args, float* partials, cudaStream_t s);
-cudaError_t launch_stream_mxfp4_down(const MxRows& h, const MxWeights& w2, const MxArgs& args, float* partials,
-                                     cudaStream_t s);
+// Both projections for at most kMxStreamRows rows (gemm_mxfp4_stream.cu).
+cudaError_t launch_stream_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
+                                    moe_act_t act, const MxRows& h, const MxArgs& args, cudaStream_t s);
 
 }  // namespace moe
