@@ -447,9 +447,10 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
         if (lead) {
           bool last = true;
           if (others > 0) {
-            last = ((*reinterpret_cast<volatile uint32_t*>(word) >> shift) & 255u) == others;
-            if (last) atomicSub(word, others << shift);
-            __threadfence();
+            uint32_t tickets;  // acquire: the pieces counted are visible
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(tickets) : "l"(word) : "memory");
+            last = ((tickets >> shift) & 255u) == others;
+            if (last) (void)atomicSub(word, others << shift);
           }
           const bool ok = mbar_wait_bounded(&tfull_bar[i & 1], (i >> 1) & 1);
           flag_s[i & 1] = (ok ? 1 : 0) | (last ? 2 : 0);
@@ -480,9 +481,11 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
           epi_barrier();
           if (lead) {
             const uint32_t before = (atomicAdd(word, 1u << shift) >> shift) & 255u;
-            if (before == others) atomicSub(word, (others + 1u) << shift);
+            if (before == others) {
+              (void)atomicSub(word, (others + 1u) << shift);
+              __threadfence();
+            }
             late_s = before == others;
-            __threadfence();
           }
           epi_barrier();
           finish = late_s != 0;
