@@ -7,7 +7,10 @@ of libmoe_b200.so (include/moe_b200.h). Importing the package loads that
 library; if it is not built the import fails.
 """
 from . import _abi  # noqa: F401  (loads libmoe_b200.so or raises)
-from ._abi import (MoeError, moe_capacity, moe_combine, moe_expert_ffn, moe_forward,  # noqa: F401
-                   moe_forward_host, moe_forward_views, moe_gather, moe_get_device_error,
-                   moe_permute, moe_route, moe_rows_max, moe_workspace_init)
+from ._abi import (MoeError, moe_capacity, moe_combine, moe_combine_backward,  # noqa: F401
+                   moe_expert_ffn, moe_expert_ffn_mxfp4, moe_forward, moe_forward_host,
+                   moe_forward_views, moe_gather, moe_gather_backward, moe_gather_mxfp4,
+                   moe_get_device_error, moe_mxfp4_dequantize_rows, moe_mxfp4_dequantize_weights,
+                   moe_mxfp4_quantize_weights, moe_permute, moe_route, moe_rows_max,
+                   moe_workspace_init, quantize_expert_weights)
 from .layer import MoeLayer  # noqa: F401

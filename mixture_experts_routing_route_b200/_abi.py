@@ -52,7 +52,8 @@ class MoeLayerC(ctypes.Structure):
                 ("act", c_int), ("capacity_factor", c_double), ("w_router", c_void_p),
                 ("router_bias", c_void_p), ("w1", c_void_p), ("w3", c_void_p), ("w2", c_void_p),
                 ("flags", c_int), ("x_router", c_void_p), ("logit_noise", c_void_p),
-                ("router_temperature", ctypes.c_float)]
+                ("router_temperature", ctypes.c_float), ("w1_scales", c_void_p),
+                ("w3_scales", c_void_p), ("w2_scales", c_void_p)]
 
 
 class MoeViewsC(ctypes.Structure):
@@ -371,9 +372,20 @@ def moe_ep_recv_plan(recv_counts, world, experts_per_rank, rows_cap, recv_rows, 
 
 
 def layer_struct(d, E, k, F, dtype, act, cf, w_router, bias, w1, w3, w2, flags=0,
-                 router_temperature=1.0) -> MoeLayerC:
+                 router_temperature=1.0, scales=(None, None, None)) -> MoeLayerC:
+    """scales: those of w1, w3 and w2 (MOE_LAYER_MXFP4)."""
     return MoeLayerC(d, E, k, F, dtype, act, float(cf), _ptr(w_router), _ptr(bias), _ptr(w1),
-                     _ptr(w3), _ptr(w2), int(flags), None, None, float(router_temperature))
+                     _ptr(w3), _ptr(w2), int(flags), None, None, float(router_temperature),
+                     *map(_ptr, scales))
+
+
+def quantize_expert_weights(w: torch.Tensor, stream=None):
+    """Expert weights [E, K, N] (bf16 or fp32, on the GPU) as MXFP4: codes [E, N, K / 2] and scales."""
+    E, K, N = w.shape
+    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(moe_mxfp4_weight_scales_size(E, K, N), dtype=torch.uint8, device=w.device)
+    moe_mxfp4_quantize_weights(w.contiguous(), E, K, N, codes, scales, stream)
+    return codes, scales
 
 
 def moe_forward_workspace_size(layer: MoeLayerC, T: int) -> int:

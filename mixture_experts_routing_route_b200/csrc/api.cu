@@ -90,7 +90,9 @@ struct FwdLayout {
   int32_t *sorted_slot, *slot_to_row, *row_slot;
   uint8_t* drop;
   int32_t* rank;
-  void *x_perm, *h, *y_perm;
+  void *x_perm, *h, *y_perm;  // MOE_LAYER_MXFP4: x_perm and h are codes
+  uint8_t *x_scales, *h_scales;  // MOE_LAYER_MXFP4
+  float* mx_partials;            // MOE_LAYER_MXFP4, decode sizes
   void *x_dev, *out_dev;  // host-buffer variant only
   int64_t cap, rows_max;
   size_t bytes;
@@ -105,6 +107,8 @@ bool gather_in_gemm(const moe_layer_t* L) {
 bool combine_in_gemm(const moe_layer_t* L) {
   return L->dtype == MOE_BF16 && L->k == 1 && (L->flags & MOE_LAYER_COMBINE_IN_GEMM) != 0;
 }
+
+bool mxfp4(const moe_layer_t* L) { return (L->flags & MOE_LAYER_MXFP4) != 0; }
 
 FwdLayout fwd_layout(const moe_layer_t* L, int T, void* ws, bool host_io) {
   FwdLayout f{};
@@ -133,8 +137,16 @@ FwdLayout fwd_layout(const moe_layer_t* L, int T, void* ws, bool host_io) {
   f.rank = static_cast<int32_t*>(c.take(permute_scratch_bytes(T, L->k, L->E)));
   // With MOE_LAYER_GATHER_IN_GEMM the up projection gathers the token rows
   // itself and there is no x_perm.
-  f.x_perm = gather_in_gemm(L) ? nullptr : c.take(R * L->d * es);
-  f.h = c.take(R * L->F * es);
+  if (mxfp4(L)) {
+    f.x_perm = c.take(R * L->d / 2);
+    f.x_scales = static_cast<uint8_t*>(c.take(moe_mxfp4_row_scales_size(f.rows_max, L->E, L->d)));
+    f.h = c.take(R * L->F / 2);
+    f.h_scales = static_cast<uint8_t*>(c.take(moe_mxfp4_row_scales_size(f.rows_max, L->E, L->F)));
+    f.mx_partials = f.rows_max <= kMxStreamRows ? static_cast<float*>(c.take(mxfp4_stream_partials_bytes())) : nullptr;
+  } else {
+    f.x_perm = gather_in_gemm(L) ? nullptr : c.take(R * L->d * es);
+    f.h = c.take(R * L->F * es);
+  }
   // With MOE_LAYER_COMBINE_IN_GEMM the down projection writes out itself.
   f.y_perm = combine_in_gemm(L) ? nullptr : c.take(R * L->d * es);
   if (host_io) {
@@ -145,6 +157,15 @@ FwdLayout fwd_layout(const moe_layer_t* L, int T, void* ws, bool host_io) {
   return f;
 }
 
+// The MXFP4 products count rows, scale tiles and stages in 32 bits.
+moe_status_t check_mxfp4_tiles(int64_t rows_max, int d, int F, int E) {
+  const int64_t kd = d / 128, kf = F / 128;
+  if (kd > 8192 || kf > 8192 || E * kd * kf >= INT_MAX || static_cast<int64_t>(E) * std::max(d, F) >= INT_MAX ||
+      rows_max >= INT_MAX || (rows_max / 128 + E) * std::max(kd, kf) >= INT_MAX)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 moe_status_t check_layer(const moe_layer_t* L, int T) {
   if (L == nullptr) return MOE_ERR_NULL;
   MOE_CHECK(check_dims(L->dtype, T, L->d, L->E, L->k));
@@ -153,8 +174,18 @@ moe_status_t check_layer(const moe_layer_t* L, int T) {
   if (!std::isfinite(L->capacity_factor)) return MOE_ERR_INVALID;
   if (!(L->router_temperature >= 0.0f) || !std::isfinite(L->router_temperature)) return MOE_ERR_INVALID;
   if ((L->flags & ~(MOE_LAYER_GATHER_IN_GEMM | MOE_LAYER_BINNED | MOE_LAYER_Z_LOSS |
-                    MOE_LAYER_COMBINE_IN_GEMM)) != 0)
+                    MOE_LAYER_COMBINE_IN_GEMM | MOE_LAYER_MXFP4)) != 0)
     return MOE_ERR_INVALID;
+  if (mxfp4(L)) {
+    if (L->dtype != MOE_BF16 || (L->flags & (MOE_LAYER_GATHER_IN_GEMM | MOE_LAYER_COMBINE_IN_GEMM)) != 0)
+      return MOE_ERR_UNSUPPORTED;
+    const int64_t cap = moe_capacity(L->capacity_factor, T, L->k, L->E);
+    MOE_CHECK(check_mxfp4_tiles(binned(L) ? moe_rows_max_binned(T, L->k, L->E, cap) : moe_rows_max(T, L->k, L->E, cap),
+                                L->d, L->F, L->E));
+    MOE_NEED(L->w1_scales);
+    MOE_NEED(L->w2_scales);
+    if (L->act == MOE_ACT_SWIGLU) MOE_NEED(L->w3_scales);
+  }
   MOE_OPT(L->x_router);
   MOE_OPT(L->logit_noise);
   if ((L->flags & MOE_LAYER_GATHER_IN_GEMM) && L->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
@@ -193,15 +224,28 @@ moe_status_t run_forward(const moe_layer_t* L, const void* x, int T, void* out, 
                                      defer != nullptr && defer->pending ? defer : nullptr)));
   rec(2);
   const bool cig = combine_in_gemm(L);
+  const MxRows xq{static_cast<uint8_t*>(f.x_perm), f.x_scales}, hq{static_cast<uint8_t*>(f.h), f.h_scales};
+  if (mxfp4(L))
+    MOE_CHECK(from_cuda(launch_gather_mxfp4(x, L->dtype, T, L->d, L->k, f.slot_to_row, f.seg, L->E, f.rows_max,
+                                            xq.codes, xq.scales, f.ctl, s)));
   // the gather kernel also zeroes the output rows of fully dropped tokens
   // when the down projection writes out
-  if (!gather_in_gemm(L) || cig)
+  else if (!gather_in_gemm(L) || cig)
     MOE_CHECK(from_cuda(launch_gather(x, es, T, L->d, L->k, f.row_slot, f.seg, L->E, f.rows_max,
                                       f.x_perm, f.ctl, s, binned(L), cig ? f.slot_to_row : nullptr,
                                       cig ? out : nullptr)));
   rec(3);
   cudaEvent_t after_up = (ev != nullptr) ? reinterpret_cast<cudaEvent_t>(ev[4]) : nullptr;
-  if (L->dtype == MOE_BF16) {
+  if (mxfp4(L)) {
+    auto weights = [](const void* c, const void* sc) {
+      return MxWeights{static_cast<const uint8_t*>(c), static_cast<const uint8_t*>(sc)};
+    };
+    // the permute, which wrote the segments, was complete before the gather began
+    MOE_CHECK(from_cuda(launch_ffn_mxfp4(xq, weights(L->w1, L->w1_scales), weights(L->w3, L->w3_scales),
+                                         weights(L->w2, L->w2_scales), L->act, f.rows_max, L->d, L->F, L->E, f.seg,
+                                         binned(L) ? f.kept : nullptr, hq, f.y_perm, f.mx_partials, f.ctl, s, after_up,
+                                         /*early_up=*/true)));
+  } else if (L->dtype == MOE_BF16) {
     const bool g = gather_in_gemm(L);
     const CombineOut co{f.row_slot, f.w, out, T};
     MOE_CHECK(from_cuda(launch_ffn_bf16(g ? x : f.x_perm, g ? T : f.rows_max,
@@ -565,15 +609,6 @@ static moe_status_t check_mxfp4(moe_dtype_t dtype, int E, int K, int N) {
   if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_INVALID;
   if (E < 1 || E > 256 || K <= 0 || N <= 0) return MOE_ERR_INVALID;
   if (K % 128 != 0 || N % 128 != 0) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-// The products count rows, scale tiles and stages in 32 bits.
-static moe_status_t check_mxfp4_tiles(int64_t rows_max, int d, int F, int E) {
-  const int64_t kd = d / 128, kf = F / 128;
-  if (kd > 8192 || kf > 8192 || E * kd * kf >= INT_MAX || static_cast<int64_t>(E) * std::max(d, F) >= INT_MAX ||
-      (rows_max / 128 + E) * std::max(kd, kf) >= INT_MAX)
-    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

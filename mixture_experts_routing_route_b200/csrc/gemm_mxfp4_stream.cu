@@ -106,6 +106,12 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t 
                    reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1) : "memory");
 }
 
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory"); }
 
 template <int UP>
@@ -166,6 +172,16 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&item_empty[slot & 1]);
     return v;
+  };
+
+  // Wait until every range of the up projection is done: h is complete, and
+  // tickets and pieces are free for the down projection.
+  auto up_done = [&]() -> bool {
+    const uint64_t limit = wait_limit_ns(args.ctl), t0 = globaltimer_ns();
+    for (;;) {
+      if (load_acquire(&args.ctl->stream_up_done) >= static_cast<unsigned>(up.W)) return true;
+      if (globaltimer_ns() - t0 > limit) return false;
+    }
   };
 
   if (warp == 0) {
@@ -306,18 +322,7 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
         ok = stream(down, item - up.W, std::integral_constant<int, 1>{}, true, [&]() -> bool {
           if (!waited) pdl_begin();
           waited = true;
-          // h is complete once every range of the up projection is done
-          const uint64_t limit = wait_limit_ns(args.ctl), t0 = globaltimer_ns();
-          bool there = true;
-          unsigned n;
-          for (;;) {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(&args.ctl->stream_up_done) : "memory");
-            if (n >= static_cast<unsigned>(up.W)) break;
-            if (globaltimer_ns() - t0 > limit) {
-              there = false;
-              break;
-            }
-          }
+          const bool there = up_done();
           // h was written by ordinary stores and is read by TMA
           asm volatile("fence.proxy.async;" ::: "memory");
           if (__all_sync(0xffffffffu, there)) return true;
@@ -445,14 +450,15 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
         // one thread decides for the four warps, which share barriers and so
         // have to leave together
         if (lead) {
-          bool last = true;
+          bool last = true, ok = true;
           if (others > 0) {
-            uint32_t tickets;  // acquire: the pieces counted are visible
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(tickets) : "l"(word) : "memory");
-            last = ((tickets >> shift) & 255u) == others;
+            // the up projection's tiles count in the same bytes
+            if (EPI == EPI_STORE) ok = up_done();
+            // acquire: the pieces counted are visible
+            last = ok && ((load_acquire(word) >> shift) & 255u) == others;
             if (last) (void)atomicSub(word, others << shift);
           }
-          const bool ok = mbar_wait_bounded(&tfull_bar[i & 1], (i >> 1) & 1);
+          if (ok) ok = mbar_wait_bounded(&tfull_bar[i & 1], (i >> 1) & 1);
           flag_s[i & 1] = (ok ? 1 : 0) | (last ? 2 : 0);
         }
         epi_barrier();

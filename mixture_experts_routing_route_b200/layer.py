@@ -19,7 +19,8 @@ class MoeLayer:
                  w3: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                  k: int = 2, act: str = "swiglu", capacity_factor: float = 0.0,
                  gather_in_gemm: bool = False, binned: bool = False, z_loss: bool = False,
-                 combine_in_gemm: bool = False, router_temperature: float = 1.0):
+                 combine_in_gemm: bool = False, router_temperature: float = 1.0,
+                 mxfp4: bool = False):
         if not w1.is_cuda:
             raise ValueError("weights must be CUDA tensors")
         self.E, self.d, self.F = w1.shape
@@ -28,9 +29,23 @@ class MoeLayer:
         self.act = abi.MOE_ACT_SWIGLU if act == "swiglu" else abi.MOE_ACT_GELU
         self.cf = float(capacity_factor)
         self.w_router = w_router.contiguous()
-        self.w1 = w1.contiguous()
-        self.w3 = None if w3 is None else w3.contiguous()
-        self.w2 = w2.contiguous()
+        # mxfp4: the experts in microscaled 4-bit floating point
+        # (MOE_LAYER_MXFP4); the weights given (bf16 or fp32) are quantised here
+        # and only their codes and scales are kept. x and out are bf16.
+        self.mxfp4 = mxfp4
+        if mxfp4:
+            self.dtype = torch.bfloat16
+            self.w1, s1 = abi.quantize_expert_weights(w1)
+            self.w3, s3 = (None, None) if w3 is None else abi.quantize_expert_weights(w3)
+            self.w2, s2 = abi.quantize_expert_weights(w2)
+            self.scales = (s1, s3, s2)
+            if w_router.dtype != torch.bfloat16:
+                raise ValueError("w_router must be bf16 with mxfp4 experts")
+        else:
+            self.w1 = w1.contiguous()
+            self.w3 = None if w3 is None else w3.contiguous()
+            self.w2 = w2.contiguous()
+            self.scales = (None, None, None)
         self.bias = None if bias is None else bias.to(device=w1.device, dtype=torch.float32).contiguous()
         # gather_in_gemm: the up projection gathers x rows itself (bf16; see
         # MOE_LAYER_GATHER_IN_GEMM in include/moe_b200.h)
@@ -40,12 +55,13 @@ class MoeLayer:
         # the top-k weight and writes out (MOE_LAYER_COMBINE_IN_GEMM)
         flags = (abi.MOE_LAYER_GATHER_IN_GEMM if gather_in_gemm else 0) | \
             (abi.MOE_LAYER_BINNED if binned else 0) | (abi.MOE_LAYER_Z_LOSS if z_loss else 0) | \
-            (abi.MOE_LAYER_COMBINE_IN_GEMM if combine_in_gemm else 0)
+            (abi.MOE_LAYER_COMBINE_IN_GEMM if combine_in_gemm else 0) | \
+            (abi.MOE_LAYER_MXFP4 if mxfp4 else 0)
         # router_temperature: the router softmax sees logits / tau (training
         # variant; moe_route_train in include/moe_b200.h)
         self.c = abi.layer_struct(self.d, self.E, k, self.F, abi.dtype_code(self.dtype), self.act,
                                   self.cf, self.w_router, self.bias, self.w1, self.w3, self.w2,
-                                  flags, router_temperature)
+                                  flags, router_temperature, self.scales)
         self._ws = {}
 
     def workspace(self, T: int, host_io: bool = False, stream=None, slot: int = 0) -> torch.Tensor:
@@ -120,8 +136,11 @@ class MoeLayer:
             "row_slot": view(v.row_slot, R, torch.int32, (R,)),
             "drop": view(v.drop_mask, S, torch.uint8, (S,)),
             # no x_perm when the up projection gathers x rows itself
-            "x_perm": view(v.x_perm, R * self.d, self.dtype, (R, self.d)) if v.x_perm else None,
-            "h": view(v.h, R * self.F, self.dtype, (R, self.F)),
+            # (mxfp4: x_perm and h are the rows' codes, two to a byte)
+            "x_perm": (view(v.x_perm, R * self.d // 2, torch.uint8, (R, self.d // 2)) if self.mxfp4 else
+                       view(v.x_perm, R * self.d, self.dtype, (R, self.d)) if v.x_perm else None),
+            "h": (view(v.h, R * self.F // 2, torch.uint8, (R, self.F // 2)) if self.mxfp4 else
+                  view(v.h, R * self.F, self.dtype, (R, self.F))),
             # no y_perm when the down projection writes the output itself
             "y_perm": view(v.y_perm, R * self.d, self.dtype, (R, self.d)) if v.y_perm else None,
             "rows_max": R,
