@@ -127,37 +127,64 @@ dequantize_weights(const uint8_t* __restrict__ codes, const uint8_t* __restrict_
   }
   T* dst = w + (static_cast<size_t>(e) * K + k0 + kb * 32) * N + n0 + 2 * c;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float a = e2m1_value((q[0][i >> 3] >> (4 * (i & 7))) & 15u) * f[0];
-    const float b = e2m1_value((q[1][i >> 3] >> (4 * (i & 7))) & 15u) * f[1];
-    *reinterpret_cast<typename Pair<T>::Raw*>(dst + static_cast<size_t>(i) * N) = Pair<T>::raw(a, b);
+  for (int g = 0; g < 4; ++g) {
+    float a[8], b[8];
+    e2m1x8_values(q[0][g], f[0], a);
+    e2m1x8_values(q[1][g], f[1], b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<typename Pair<T>::Raw*>(dst + static_cast<size_t>(8 * g + i) * N) = Pair<T>::raw(a[i], b[i]);
   }
 }
 
-// Eight consecutive values of a row.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive values of a row: as loaded, as fp32, the fp32 bits of the
+// largest magnitude.
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+  struct Raw { uint4 u; };
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) { return {__ldg(reinterpret_cast<const uint4*>(p))}; }
+  static __device__ __forceinline__ Raw zero() { return {make_uint4(0, 0, 0, 0)}; }
+  static __device__ __forceinline__ void f32(const Raw& r, float (&v)[8]) {
+    const uint32_t x[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(x[i] << 16);
-    v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(x[i] << 16);
+      v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(Pair<__nv_bfloat16>::raw(v[0], v[1]), Pair<__nv_bfloat16>::raw(v[2], v[3]),
-                                            Pair<__nv_bfloat16>::raw(v[4], v[5]), Pair<__nv_bfloat16>::raw(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
-}
+  static __device__ __forceinline__ uint32_t top(const Raw& r) {
+    constexpr uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(r.u.x & m, r.u.y & m), __vmaxu2(r.u.z & m, r.u.w & m));
+    return max(t & 0xffff0000u, t << 16);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
+    using P = Pair<__nv_bfloat16>;
+    *reinterpret_cast<uint4*>(p) = make_uint4(P::raw(v[0], v[1]), P::raw(v[2], v[3]), P::raw(v[4], v[5]), P::raw(v[6], v[7]));
+  }
+};
+template <> struct Eight<float> {
+  struct Raw { float4 a, b; };
+  static __device__ __forceinline__ Raw load(const float* p) {
+    return {__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1)};
+  }
+  static __device__ __forceinline__ Raw zero() { return {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)}; }
+  static __device__ __forceinline__ void f32(const Raw& r, float (&v)[8]) {
+    v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+    v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+  }
+  static __device__ __forceinline__ uint32_t top(const Raw& r) {
+    float v[8];
+    f32(r, v);
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7fffffffu);
+    return t;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
 
 constexpr int kRowWarps = 8;
 constexpr int kRowIter = 4;                  // a unit: 4 x 256 values of one row
@@ -196,30 +223,25 @@ gather_mxfp4(const T* __restrict__ x, int T_, int d, int k, const int32_t* __res
   for (long long u = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
     const long long t = u / chunks;
     const int c0 = static_cast<int>(u - t * chunks) * kRowChunk;
-    float v[kRowIter][8];
+    typename Eight<T>::Raw raw[kRowIter];  // all loads of the unit before the first use
 #pragma unroll
     for (int i = 0; i < kRowIter; ++i) {
       const int col = c0 + i * 256 + lane * 8;
-      if (col < d) {
-        load8(x + static_cast<size_t>(t) * d + col, v[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-      }
+      raw[i] = col < d ? Eight<T>::load(x + static_cast<size_t>(t) * d + col) : Eight<T>::zero();
     }
     uint32_t q[kRowIter], sw[kRowIter];  // codes; scale bytes of the lane's four neighbouring blocks
 #pragma unroll
     for (int i = 0; i < kRowIter; ++i) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+      uint32_t top = Eight<T>::top(raw[i]);
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const uint32_t sb = mx_scale_byte(top);
       const float inv = mx_inv_scale(sb);
+      float v[8];
+      Eight<T>::f32(raw[i], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-      q[i] = sb == 255u ? 0u : e2m1x8(v[i]);
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
+      q[i] = sb == 255u ? 0u : e2m1x8(v);
       sw[i] = sb << (8 * ((lane >> 2) & 3));
       sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
       sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
@@ -292,11 +314,9 @@ dequantize_rows(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ s
     for (int i = 0; i < kRowIter; ++i) {
       const int col = c0 + i * 256 + lane * 8;
       if (col >= K) continue;
-      const float f = mx_scale(sb[i]);
       float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e2m1_value((q[i] >> (4 * j)) & 15u) * f;
-      store8(out + static_cast<size_t>(row) * K + col, v);
+      e2m1x8_values(q[i], mx_scale(sb[i]), v);
+      Eight<T>::store(out + static_cast<size_t>(row) * K + col, v);
     }
   }
 }

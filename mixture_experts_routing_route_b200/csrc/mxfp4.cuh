@@ -19,6 +19,7 @@
 // floor((a + n) / 128) + 1 >= floor(a / 128) + ceil(n / 128)).
 #pragma once
 #include "common.cuh"
+#include <cuda_fp16.h>
 
 namespace moe {
 
@@ -68,12 +69,24 @@ __device__ __forceinline__ uint32_t e2m1(float v) {
   return r;
 }
 
-// Value of one code (0..15) at scale 1.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  // 0, .5: m * .5; else (1 + (m & 1) / 2) * 2^((m >> 1) - 1), built as fp32 bits
-  const uint32_t bits = m < 2u ? (m == 0u ? 0u : 0x3f000000u) : (((m >> 1) + 126u) << 23) | ((m & 1u) << 22);
-  return __uint_as_float(bits | ((c & 8u) << 28));
+// Eight codes (the first in the lowest four bits) to their values times f:
+// through fp16, which holds every E2M1 value exactly.
+__device__ __forceinline__ void e2m1x8_values(uint32_t codes, float f, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = p.x * f;
+    v[2 * i + 1] = p.y * f;
+  }
 }
 
 // Byte offset of the scale of (row group, row in the group, block) among
