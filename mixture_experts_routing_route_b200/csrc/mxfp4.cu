@@ -190,6 +190,7 @@ constexpr int kRowWarps = 8;
 constexpr int kRowIter = 4;                  // a unit: 4 x 256 values of one row
 constexpr int kRowChunk = kRowIter * 256;
 constexpr int kRowMaxE = 256;
+constexpr int kGatherBlocksPerSm = 5;        // 48 registers
 
 // Expert of row r: the last e with seg[e] <= r (empty experts share a start
 // with the one that has the row). Valid for seg[0] <= r < seg[E].
@@ -207,7 +208,7 @@ __device__ __forceinline__ int row_expert(const int* seg, int E, int r) {
 // hold a block (8 values a lane), so a block's largest magnitude is two
 // shuffles away, and a lane's codes are one 4-byte store of a 128-byte run.
 template <typename T>
-__global__ void __launch_bounds__(kRowWarps * 32)
+__global__ void __launch_bounds__(kRowWarps * 32, kGatherBlocksPerSm)
 gather_mxfp4(const T* __restrict__ x, int T_, int d, int k, const int32_t* __restrict__ slot_to_row,
              const int32_t* __restrict__ seg, int E, long long rows_max, uint8_t* __restrict__ codes,
              uint8_t* __restrict__ scales, Control* ctl) {
@@ -223,11 +224,25 @@ gather_mxfp4(const T* __restrict__ x, int T_, int d, int k, const int32_t* __res
   for (long long u = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5); u < units; u += step) {
     const long long t = u / chunks;
     const int c0 = static_cast<int>(u - t * chunks) * kRowChunk;
+    // lane j: the token's j-th row
+    const int row = lane < k ? __ldg(slot_to_row + t * k + lane) : -1;
     typename Eight<T>::Raw raw[kRowIter];  // all loads of the unit before the first use
 #pragma unroll
     for (int i = 0; i < kRowIter; ++i) {
       const int col = c0 + i * 256 + lane * 8;
       raw[i] = col < d ? Eight<T>::load(x + static_cast<size_t>(t) * d + col) : Eight<T>::zero();
+    }
+    // where that row's codes and scales begin; -1: none
+    long long code_at = -1, scale_at = 0;
+    if (row >= 0) {
+      const int e = row_expert(seg_s, E, row);
+      const int rank = row - seg_s[e];
+      if (row >= R || rank < 0 || seg_s[e] < 0) {  // out of range, or seg is not an ascending list from 0
+        set_error(ctl, MOE_DEVERR_ROW_RANGE);
+      } else {
+        code_at = static_cast<long long>(row) * (d / 2);
+        scale_at = static_cast<long long>(mx_scale_at(seg_s[e] / 128 + e + rank / 128, d / 128, rank & 127, 0));
+      }
     }
     uint32_t q[kRowIter], sw[kRowIter];  // codes; scale bytes of the lane's four neighbouring blocks
 #pragma unroll
@@ -247,26 +262,15 @@ gather_mxfp4(const T* __restrict__ x, int T_, int d, int k, const int32_t* __res
       sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
     }
     for (int j = 0; j < k; ++j) {
-      const int row = __ldg(slot_to_row + t * k + j);
-      if (row < 0) continue;
-      if (row >= R) {
-        if (lane == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
-        continue;
-      }
-      const int e = row_expert(seg_s, E, row);
-      const int rank = row - seg_s[e];
-      if (rank < 0 || seg_s[e] < 0) {  // seg is not an ascending list from 0
-        if (lane == 0) set_error(ctl, MOE_DEVERR_ROW_RANGE);
-        continue;
-      }
-      const long long group = seg_s[e] / 128 + e + rank / 128;
+      const long long cj = __shfl_sync(0xffffffffu, code_at, j), sj = __shfl_sync(0xffffffffu, scale_at, j);
+      if (cj < 0) continue;
+      uint8_t* cdst = codes + cj + c0 / 2 + lane * 4;
+      uint8_t* sdst = scales + sj + (c0 / 128 + (lane >> 4)) * kScaleTile;
 #pragma unroll
       for (int i = 0; i < kRowIter; ++i) {
-        const int col = c0 + i * 256 + lane * 8;
-        if (col >= d) continue;
-        *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(row) * (d / 2) + col / 2) = q[i];
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(scales + mx_scale_at(group, d / 128, rank & 127, col / 32)) = sw[i];
+        if (c0 + i * 256 + lane * 8 >= d) continue;
+        *reinterpret_cast<uint32_t*>(cdst + i * 128) = q[i];
+        if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(sdst + i * 2 * kScaleTile) = sw[i];
       }
     }
   }
@@ -321,8 +325,11 @@ dequantize_rows(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ s
   }
 }
 
-int row_grid(long long units) {
-  return static_cast<int>(std::max<long long>(1, std::min<long long>((units + kRowWarps - 1) / kRowWarps, 8LL * num_sms())));
+// Blocks for so many units (a warp each): at most what is resident at once,
+// since every block takes an equal share.
+int row_grid(long long units, int per_sm) {
+  return static_cast<int>(
+      std::max<long long>(1, std::min<long long>((units + kRowWarps - 1) / kRowWarps, static_cast<long long>(per_sm) * num_sms())));
 }
 
 }  // namespace
@@ -351,7 +358,7 @@ cudaError_t launch_gather_mxfp4(const void* x, moe_dtype_t dt, int T, int d, int
                                 const int32_t* slot_to_row, const int32_t* seg, int E, int64_t rows_max,
                                 uint8_t* codes, uint8_t* scales, Control* ctl, cudaStream_t s) {
   if (T <= 0 || rows_max <= 0) return cudaSuccess;
-  const int grid = row_grid(static_cast<long long>(T) * ((d + kRowChunk - 1) / kRowChunk));
+  const int grid = row_grid(static_cast<long long>(T) * ((d + kRowChunk - 1) / kRowChunk), kGatherBlocksPerSm);
   if (dt == MOE_BF16)
     return launch_pdl(gather_mxfp4<__nv_bfloat16>, dim3(grid), dim3(kRowWarps * 32), 0, s, false,
                       static_cast<const __nv_bfloat16*>(x), T, d, k, slot_to_row, seg, E, rows_max, codes,
@@ -364,7 +371,7 @@ cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* sc
                                          int E, int64_t rows_max, int K, moe_dtype_t dt, void* out,
                                          Control* ctl, cudaStream_t s) {
   if (rows_max <= 0) return cudaSuccess;
-  const int grid = row_grid(rows_max * ((K + kRowChunk - 1) / kRowChunk));
+  const int grid = row_grid(rows_max * ((K + kRowChunk - 1) / kRowChunk), 8);
   if (dt == MOE_BF16)
     return launch_pdl(dequantize_rows<__nv_bfloat16>, dim3(grid), dim3(kRowWarps * 32), 0, s, false, codes,
                       scales, seg, E, rows_max, K, static_cast<__nv_bfloat16*>(out), ctl);
