@@ -187,10 +187,10 @@ template <> struct Eight<float> {
 };
 
 constexpr int kRowWarps = 8;
-constexpr int kRowIter = 4;                  // a unit: 4 x 256 values of one row
+constexpr int kRowIter = 8;                  // a unit: 8 x 256 values of one row (4: 8% slower at d = 4096, 2: 35%)
 constexpr int kRowChunk = kRowIter * 256;
 constexpr int kRowMaxE = 256;
-constexpr int kGatherBlocksPerSm = 5;        // 48 registers
+constexpr int kGatherBlocksPerSm = 3;        // by registers
 
 // Expert of row r: the last e with seg[e] <= r (empty experts share a start
 // with the one that has the row). Valid for seg[0] <= r < seg[E].
@@ -203,7 +203,7 @@ __device__ __forceinline__ int row_expert(const int* seg, int E, int r) {
   return lo;
 }
 
-// The rows on their way to the experts: a warp takes 1024 values of one token,
+// The rows on their way to the experts: a warp takes 2048 values of one token,
 // quantises them once and writes them to each of the token's rows. Four lanes
 // hold a block (8 values a lane), so a block's largest magnitude is two
 // shuffles away, and a lane's codes are one 4-byte store of a 128-byte run.
