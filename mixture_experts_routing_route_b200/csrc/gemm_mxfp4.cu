@@ -78,9 +78,12 @@ struct Cfg {
 
 // 32 fp32 values (one block) of a row to 16 bytes of codes; returns the scale byte.
 __device__ __forceinline__ uint32_t quantise_block(float (&h)[32], uint4& codes) {
-  uint32_t top = 0;
+  // two values an instruction; a NaN stays one
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(h[i]) & 0x7fffffffu);
+  for (int i = 0; i < 32; i += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(h[i]), "f"(h[i + 1]));
+  const uint32_t top = __float_as_uint(m) & 0x7fffffffu;
   const uint32_t sb = mx_scale_byte(top);
   const float inv = mx_inv_scale(sb);
   uint32_t q[4];
@@ -88,7 +91,11 @@ __device__ __forceinline__ uint32_t quantise_block(float (&h)[32], uint4& codes)
   for (int g = 0; g < 4; ++g) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = h[8 * g + i] * inv;
+    for (int i = 0; i < 8; i += 2) {
+      const float2 p = unpack2(mul2(pack2(h[8 * g + i], h[8 * g + i + 1]), pack2(inv, inv)));
+      v[i] = p.x;
+      v[i + 1] = p.y;
+    }
     q[g] = sb == 255u ? 0u : e2m1x8(v);
   }
   codes = make_uint4(q[0], q[1], q[2], q[3]);
@@ -123,8 +130,12 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
       tmem_ld_wait();
       if (gi == 0) free_overlap();
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        h[i] = EPI == EPI_GELU ? gelu_fast(__uint_as_float(v[i])) : __uint_as_float(v[i]);
+      for (int i = 0; i < 32; i += 2) {
+        const float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
+        const float2 r = EPI == EPI_GELU ? gelu_fast2(a, b) : make_float2(a, b);
+        h[i] = r.x;
+        h[i + 1] = r.y;
+      }
     }
     const int col = t.n0 + 32 * g;
     if constexpr (EPI == EPI_STORE) {
