@@ -12,27 +12,25 @@
 // The two CTAs of a cluster compute one 256-row x N tile together
 // (cta_group::2), persistently. CTA r holds A rows [row0 + 128 r, +128) and its
 // half of the B columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output
-// columns), its rows' scales and the scales of all B columns. Eleven warps a CTA:
+// columns), its rows' scales and the scales of all B columns. Its warps:
 //   warp 0   producer: per stage (256 values of K) the A and B boxes by TMA (128
 //            bytes = 256 codes a row, 128-byte swizzle) and the scale tiles (two
 //            of 512 bytes per 128 rows)
 //   warp 1   MMA issuer (even CTA): per 128 values of K one thread copies the
 //            scale tiles to tensor memory of both CTAs (tcgen05.cp, replicated
 //            to the four lane quarters) and issues two MMAs of K = 64
-//   warps 2-9 epilogue: a thread per row and half of the columns, 32 columns
-//            (one block) at a time; two warps per scheduler hide the latency of
-//            the activation's exponentials
-// Why pairs: an SM takes about 52 bytes per clock from L2 (measured), and a
-// 128 x 256 tile of one CTA needs 48 KB of operands per 512 clocks of MMA, 94
-// bytes per clock; a pair's CTA needs 35 KB.
+//   8 or 16  epilogue: a thread per row and a half or a quarter of the columns,
+//            32 columns (one block) at a time
+//   the last scheduler: hands out tiles
+// Why pairs: a 128 x 256 tile of one CTA needs 51 KB from L2 per 512 clocks of
+// MMA, 100 bytes per clock and SM; a pair's CTA needs 35 KB, which it gets: a
+// stage takes 525 to 540 clocks (K = 4096 and 14336).
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit in
 // 512 columns, so the accumulators overlap by 32 columns (columns 0-255 and
 // 224-479) and the scales use 480-511 (two sets of 12, taken in turn). The
 // epilogue reads the overlapping columns first and frees them at once; the
 // next tile's MMAs start then, while the rest of the tile is still read.
-//
-//   warp 10  scheduler: hands out tiles
 //
 // Work is handed out dynamically, as in the bf16 CTA-pair kernel, so that pairs
 // sharing a weight block read it at nearly the same time: the even CTA's
@@ -50,10 +48,7 @@ namespace moe {
 namespace {
 
 constexpr int kTileM = 256;
-constexpr int kEpiWarps = 8;               // per CTA
-constexpr int kThreads = 64 + 32 * kEpiWarps + 32;
 constexpr int kUnitSlots = 3;              // ring of tiles published to a CTA's roles
-constexpr uint32_t kUnitReaders = 1 + kEpiWarps;  // producer, epilogue warps (and the even CTA's MMA warp)
 
 // Arrive on another CTA's mbarrier without a release: for arrivals that order
 // tensor-memory loads only (complete, and fenced by tcgen05.fence).
@@ -73,6 +68,15 @@ struct Cfg {
   static constexpr int ACC1 = NMMA == 256 ? 224 : 128;   // first column of the second accumulator
   static constexpr int SF_COL = 480;
   static constexpr int TMEM_COLS = 512;
+  // epilogue warps: four lane quarters x PARTS of the columns. GELU: the
+  // activation bounds short K, and four warps a scheduler hide its latencies
+  // (capacity workload 106 -> 102 us); elsewhere they cost (Mixtral-shaped 574
+  // -> 601 us: more warps waiting on shared memory beside the MMAs).
+  static constexpr int PARTS = EPI == EPI_GELU ? 4 : 2;
+  static constexpr int EPI_WARPS = 4 * PARTS;
+  static constexpr int SCHED_WARP = 2 + EPI_WARPS;
+  static constexpr int THREADS = 32 * (SCHED_WARP + 1);
+  static constexpr uint32_t UNIT_READERS = 1 + EPI_WARPS;  // producer, epilogue warps (and the even CTA's MMA warp)
   static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE_BYTES + 1024;
 };
 
@@ -157,15 +161,15 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
     if (valid) {
       const int r = crow + lane;
       uint8_t* dst = args.out_scales + mx_scale_at(t.group + r / 128, args.N / 128, r & 127, t.n0 / 32 + g0);
-      static_assert(G == 2 || G == 4, "half of 128 or of 256 columns");
-      if constexpr (G == 4) *reinterpret_cast<uint32_t*>(dst) = sw;
-      else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sw);
+      static_assert(G == 1 || G == 2, "a part of 128 or of 256 columns");
+      if constexpr (G == 2) *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sw);
+      else *dst = static_cast<uint8_t>(sw);
     }
   }
 }
 
 template <int EPI, int NMMA>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<EPI, NMMA>::THREADS, 1)
 grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmSA,
                   const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1, MxArgs args) {
@@ -193,10 +197,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   if (threadIdx.x == 0) {
     abort_s = 0;
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * kEpiWarps); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * C::EPI_WARPS); }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
-      mbar_init(&unit_empty[i], kUnitReaders + (rank == 0 ? 1 : 0));
+      mbar_init(&unit_empty[i], C::UNIT_READERS + (rank == 0 ? 1 : 0));
       mbar_init(&peer_full[i], 1);
       mbar_init(&peer_empty[i], 1);
     }
@@ -207,7 +211,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     tmem_alloc_pair(&tmem_base_s, C::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  if (warp == 10 && lane == 0) {
+  if (warp == C::SCHED_WARP && lane == 0) {
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB0);
     prefetch_tmap(&tmB1);
@@ -260,7 +264,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     return t.rows > 0;
   };
 
-  if (warp == 10) {
+  if (warp == C::SCHED_WARP) {
     TileList<kTileM> list;
     load_segments(segments, args, lane, 32);
     __syncwarp();
@@ -460,11 +464,11 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
     }
   } else {
-    // epilogue warps 2..9: tensor-memory lane quarter = warp % 4 of this CTA's
-    // 128 rows, first or second half of the column groups
-    constexpr int G = C::OUT_N / 64;  // groups of 32 columns per warp
+    // epilogue warps: tensor-memory lane quarter = warp % 4 of this CTA's 128
+    // rows, and a part of the column groups
+    constexpr int G = C::OUT_N / 32 / C::PARTS;  // groups of 32 columns per warp
     if (early) pdl_begin();
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, part = (warp - 2) >> 2;
     int uslot = 0;
     uint32_t uphase = 0;
     for (int i = 0;; ++i) {
@@ -478,9 +482,13 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         __syncwarp();
         if (lane == 0) arrive_relaxed_cluster(tfree0 + acc * 8u);
       };
+      const int crow = 128 * static_cast<int>(rank) + q * 32;
       // The shared columns are in the last group of the first accumulator
-      // (second half's warps) and in the first group of the second.
-      epilogue<EPI, C::OUT_N, G>(tbase, args, t, 128 * static_cast<int>(rank) + q * 32, lane, half * G, acc == 0,
+      // (last part's warps) and in the first group of the second. A warp
+      // without rows leaves the others its issue slots (a skewed layer's last
+      // tiles have few rows: capacity workload 108 -> 106 us).
+      if (crow >= t.rows) free_overlap();
+      else epilogue<EPI, C::OUT_N, G>(tbase, args, t, crow, lane, part * G, acc == 0,
                                  free_overlap);
     }
   }
@@ -509,7 +517,7 @@ cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, 
   auto kern = grouped_gemm_mxf4<EPI, NMMA>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   const int pairs = num_sms() / 2;
-  return launch_pdl_cluster(kern, dim3(2 * pairs), dim3(kThreads), C::SMEM, s, 2, ta, tb0, tb1, sa, sb0, sb1, args);
+  return launch_pdl_cluster(kern, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, s, 2, ta, tb0, tb1, sa, sb0, sb1, args);
 }
 
 }  // namespace
@@ -535,7 +543,7 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.out_scales = h.scales;
   a.out = static_cast<__nv_bfloat16*>(y);
   // A decode step's rows (32 at most, so no expert has more) go through the
-  // weight stream: one token of a Mixtral-shaped layer takes STREAM us there,
+  // weight stream: one token of a Mixtral-shaped layer takes 44 us there,
   // 57 us here.
   if (rows_max <= kMxStreamRows) {
     a.partials = partials;
