@@ -16,7 +16,9 @@
 //    order of K (the same order whoever is last: the same bits);
 //  - both projections are one launch. The down projection's first weights are
 //    loaded before h is complete, into the ring that the up projection drains.
-//    As two launches, h crossed a kernel boundary of 3 to 4 us.
+//    As two launches, h crossed a kernel boundary of 3 to 4 us. (Prefetching the
+//    rest of them to L2 as well held up the blocks still at the up projection:
+//    126 -> 136 us with all eight experts of a Mixtral-shaped layer.)
 //
 // Blocks take ranges from a counter, the up projection's first, and wait for h
 // only with a range of the down projection in hand. So whatever blocks are
@@ -98,12 +100,6 @@ __device__ __forceinline__ void load_columns(uint32_t tbase, int c, float (&v)[M
   for (int m = 0; m < MATS; ++m)
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[m][k] = __uint_as_float(r[m][k]);
-}
-
-// A tile of a tensor map to L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1) : "memory");
 }
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
@@ -271,21 +267,6 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
         __syncwarp();
         next_slot();
       }
-      // The weights of the range's other stages to L2 meanwhile: the wait costs
-      // no DRAM time then.
-      if (decltype(p)::value == 1 && weights_first)
-        for (int s = beg + ahead; s < end; ++s) {
-          const int kb = at_stage(sh, s);
-          if (elect_one()) {
-            const int row = t.e * (sh.ntn * 128) + t.n0;
-            const int n = boxes(sh, p, kb);
-            for (int j = 0; j < n; ++j) {
-              tma_prefetch_2d(&maps.w[2], (kb * C::BOXES + j) * 128, row);
-              tma_prefetch_2d(&maps.sw[2], 0, (row / 128) * sh.katoms + 2 * (kb * C::BOXES + j));
-            }
-          }
-          __syncwarp();
-        }
       const bool go = ready();
       // rows of the stages that have their weights (also after a time-out: a
       // stage armed has to complete)
