@@ -122,7 +122,8 @@ combine_bwd(const T* __restrict__ dout, const T* __restrict__ y, const float* __
 }
 
 // A thread owns two 16-byte column vectors of one token and requests its K
-// rows of both before it adds them (dx_in first, then j ascending). A token
+// rows of both before it adds them (dx_in first, then j ascending; dx may be
+// dx_in: a thread reads what it writes before it writes it). A token
 // takes tpt threads; a block takes whole tokens when tpt fits it, otherwise a
 // token spreads over grid.y.
 constexpr int kSumThreads = 128;
@@ -130,8 +131,7 @@ constexpr int kSumThreads = 128;
 template <typename T, int K>
 __global__ void __launch_bounds__(kSumThreads)
 gather_bwd(const T* __restrict__ rows_g, const int32_t* __restrict__ slot_to_row,
-           const T* __restrict__ dx_in, int T_, int d, int tpt, long long rows_max,
-           T* __restrict__ dx, Control* ctl) {
+           const T* dx_in, int T_, int d, int tpt, long long rows_max, T* dx, Control* ctl) {
   pdl_begin();
   using V = Vec<T>;
   constexpr int NV = 2;

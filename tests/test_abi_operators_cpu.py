@@ -209,3 +209,44 @@ def test_reference_quantisation():
         v[0, 3] = top
         assert R.quantise(v)[1][0, 0] == byte
     assert np.array_equal(R.unpack(R.pack(codes)), codes)
+
+
+def test_binding_refuses_host_tensors(abi):
+    """A host address would fault on the GPU: the binding refuses it before the library is called."""
+    import torch
+    f, i, u = torch.zeros(8, 128), torch.zeros(16, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8)
+    w = torch.zeros(1, 128, 128)
+    for call_ in (
+        lambda: abi.moe_combine_backward(f, f, f, i, 8, 128, 2, 16, f, f, u),
+        lambda: abi.moe_gather_backward(f, i, None, 8, 128, 2, 16, f, u),
+        lambda: abi.moe_mxfp4_quantize_weights(w, 1, 128, 128, u, u),
+        lambda: abi.moe_mxfp4_dequantize_weights(u, u, 1, 128, 128, w),
+        lambda: abi.quantize_expert_weights(w),
+        lambda: abi.moe_gather_mxfp4(f, 8, 128, 2, i, i, 4, 16, u, u, u),
+        lambda: abi.moe_mxfp4_dequantize_rows(u, u, i, 4, 16, 128, f, u),
+        lambda: abi.moe_expert_ffn_mxfp4(u, u, u, u, u, u, u, u, 1, 16, 128, 128, 4, i, u, u, u, u),
+    ):
+        with pytest.raises(ValueError, match="not on the current CUDA device"):
+            call_()
+
+
+def test_binding_refuses_other_devices_and_strides(abi, monkeypatch):
+    class Fake:
+        def __init__(self, device, contiguous=True):
+            self.device, self.ok, self.shape = device, contiguous, (2, 2)
+
+        def get_device(self):
+            return self.device
+
+        def is_contiguous(self):
+            return self.ok
+
+        def stride(self):
+            return (1, 2)
+
+    monkeypatch.setattr(abi, "_current_device", lambda: 0)
+    abi._on_gpu(Fake(0), None, Fake(0))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        abi._on_gpu(Fake(0), Fake(1))
+    with pytest.raises(ValueError, match="not contiguous"):
+        abi._on_gpu(Fake(0), Fake(0, contiguous=False))

@@ -360,3 +360,52 @@ def test_quantise_gather_ffn_combine_together():
     ref = sum(np.where(s2r[:, j] >= 0, wn[:, j], 0.0)[:, None] * yn[np.maximum(s2r[:, j], 0)] for j in range(k))
     mag = sum(np.abs(np.where(s2r[:, j] >= 0, wn[:, j], 0.0)[:, None] * yn[np.maximum(s2r[:, j], 0)]) for j in range(k))
     assert np.all(np.abs(np32(out) - ref) <= 1.01 * (2.0 ** -8 * np.abs(ref) + 2 * k * 2.0 ** -24 * mag))
+
+
+def test_offsets_past_32_bits():
+    """Codes, values and h of more than 2^32 bytes: the last rows against the same rows on their own."""
+    d, F, E, k = 8192, 8192, 2, 2
+    T = (1 << 32) * 2 // d // k + 300            # T k rows of d / 2 bytes: past 4 GiB
+    rows = T * k
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x[-300:] = torch.randn(300, d, device=DEV, generator=g)
+    s2r = torch.stack((torch.arange(T), torch.arange(T) + T), 1).to(torch.int32).to(DEV)
+    seg = torch.tensor([0, T, rows], dtype=torch.int32, device=DEV)
+    codes, scales = u8(rows * d // 2), u8(abi.moe_mxfp4_row_scales_size(rows, E, d))
+    ws = new_ws(256)
+    abi.moe_gather_mxfp4(x, T, d, k, s2r, seg, E, rows, codes, scales, ws)
+    assert abi.moe_get_device_error(ws) == 0
+    rc, _ = R.quantise(np32(x[-300:]))
+    tail = codes[-300 * (d // 2):].reshape(300, d // 2)
+    assert np.array_equal(R.unpack(npi(tail)), rc)
+    ex = Experts(E, d, F, "gelu", 3)
+    hc, hs, y, ws2 = run_ffn(ex, codes, scales, rows, seg)
+    assert abi.moe_get_device_error(ws2) == 0
+    # the last 300 rows on their own, as expert 1's only rows (the same place in their scale tiles)
+    pad = T % 128 - 300 % 128
+    n = 300 + (pad if pad >= 0 else pad + 128)
+    seg1 = torch.tensor([0, 0, n], dtype=torch.int32, device=DEV)
+    xs1 = u8(abi.moe_mxfp4_row_scales_size(n, E, d))
+    xc1 = u8(n * d // 2).reshape(n, d // 2)
+    s2r1 = torch.arange(n, dtype=torch.int32, device=DEV)
+    abi.moe_gather_mxfp4(x[-n:].contiguous(), n, d, 1, s2r1, seg1, E, n, xc1, xs1, ws)
+    _, _, y1, _ = run_ffn(ex, xc1, xs1, n, seg1)
+    assert torch.equal(y[-300:], y1[-300:])
+    assert y.shape[0] * d * 2 > 1 << 33
+    out = torch.empty(rows, d, dtype=torch.bfloat16, device=DEV)
+    abi.moe_mxfp4_dequantize_rows(codes, scales, seg, E, rows, d, out, ws)
+    assert torch.equal(out[-300:], out[T - 300:T])
+    assert np.array_equal(np32(out[-300:]).astype(np.float64), R.values(*R.quantise(np32(x[-300:]))))
+    # and the gradients' way over rows of that many bytes
+    w = torch.full((T, k), 0.5, device=DEV)
+    dw = torch.empty(T, k, device=DEV)
+    abi.moe_combine_backward(x, y, w, s2r, T, d, k, rows, out, dw, ws)
+    assert torch.equal(out[-300:], 0.5 * x[-300:]) and torch.equal(out[T - 300:T], 0.5 * x[-300:])
+    ref = (x[-300:].double() * y[-300:].double()).sum(1)
+    mag = (x[-300:].double() * y[-300:].double()).abs().sum(1)
+    assert torch.all((dw[-300:, 1].double() - ref).abs() <= 1.01 * (d + 1) * 2.0 ** -24 * mag)
+    dx = torch.empty_like(x)
+    abi.moe_gather_backward(out, s2r, None, T, d, k, rows, dx, ws)
+    assert torch.equal(dx[-300:], x[-300:])
+    assert abi.moe_get_device_error(ws) == 0

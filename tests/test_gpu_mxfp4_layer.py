@@ -126,8 +126,9 @@ def test_layer_in_a_graph_beside_the_bf16_layer():
         assert layer.device_error(T) == 0
 
 
-def test_two_layers_on_two_streams():
-    T, d, E, k, F = 2, 1024, 8, 2, 1024
+@pytest.mark.parametrize("T", [2, 300])
+def test_two_layers_on_two_streams(T):
+    d, E, k, F = 1024, 8, 2, 1024
     layers = []
     for seed in (1, 2):
         ws = weights(E, d, F, "swiglu", seed)
@@ -145,6 +146,26 @@ def test_two_layers_on_two_streams():
     for i in range(2):
         assert layers[i].device_error(T) == 0
         assert all(torch.equal(o, alone[i]) for o in got[i])
+
+
+@pytest.mark.parametrize("T", [5, 150])
+def test_host_buffers(T):
+    d, E, k, F = 256, 8, 2, 384
+    ws = weights(E, d, F, "gelu", 9)
+    layer = MoeLayer(ws[0], ws[1], ws[2], k=k, act="gelu", mxfp4=True)
+    x = tokens(T, d, 2)
+    out, aux = layer.forward(x)
+    xh, oh, ah = x.cpu().pin_memory(), torch.empty(T, d, dtype=torch.bfloat16).pin_memory(), torch.empty(1).pin_memory()
+    layer.forward_host(xh, oh, ah)
+    torch.cuda.synchronize()
+    assert torch.equal(oh, out.cpu()) and torch.equal(ah, aux.cpu())
+
+
+def test_no_tokens():
+    ws = weights(4, 128, 128, "gelu", 1)
+    layer = MoeLayer(ws[0], ws[1], ws[2], k=2, act="gelu", mxfp4=True)
+    out, _ = layer.forward(torch.empty(0, 128, dtype=torch.bfloat16, device=DEV))
+    assert out.shape == (0, 128) and layer.device_error(0) == 0
 
 
 def test_mxfp4_needs_a_bf16_router():
