@@ -9,14 +9,15 @@
 //      scales of h); or the plain bf16 store of the down projection. Sums and
 //      activations are fp32; h is rounded once (to E2M1), y once (to bf16).
 //
-// The two CTAs of a cluster compute one 256-row x N tile together
-// (cta_group::2), persistently. CTA r holds A rows [row0 + 128 r, +128) and its
+// Two forms of one kernel. GROUP 2, for experts with many rows: the two CTAs of
+// a cluster compute one 256-row x N tile together (cta_group::2). GROUP 1: a CTA
+// computes a 128-row x N tile. Both are persistent. As a pair, CTA r holds A rows [row0 + 128 r, +128) and its
 // half of the B columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output
 // columns), its rows' scales and the scales of all B columns. Its warps:
 //   warp 0   producer: per stage (256 values of K) the A and B boxes by TMA (128
 //            bytes = 256 codes a row, 128-byte swizzle) and the scale tiles (two
 //            of 512 bytes per 128 rows)
-//   warp 1   MMA issuer (even CTA): per 128 values of K one thread copies the
+//   warp 1   MMA issuer (of a pair: the even CTA's): per 128 values of K one thread copies the
 //            scale tiles to tensor memory of both CTAs (tcgen05.cp, replicated
 //            to the four lane quarters) and issues two MMAs of K = 64
 //   8 or 16  epilogue: a thread per row and a half or a quarter of the columns,
@@ -32,11 +33,11 @@
 // epilogue reads the overlapping columns first and frees them at once; the
 // next tile's MMAs start then, while the rest of the tile is still read.
 //
-// Work is handed out dynamically, as in the bf16 CTA-pair kernel, so that pairs
+// Work is handed out dynamically, as in the bf16 CTA-pair kernel, so that CTAs
 // sharing a weight block read it at nearly the same time: the even CTA's
-// scheduler takes the next tile from a counter in the control block, decodes
+// scheduler (GROUP 1: each CTA's) takes the next tile from a counter in the control block, decodes
 // it, publishes it to its CTA's roles and hands it to the odd CTA's scheduler,
-// which does the same there. The three-slot ring keeps this chain (some 3000
+// if there is one, which does the same there. The three-slot ring keeps this chain (some 3000
 // cycles a tile: the counter, a search with a division, waits and releases at
 // cluster scope) off every other role's path, and takes no tile so early that
 // a slow pair would hold work an idle one could do.
@@ -47,7 +48,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kTileM = 256;
 constexpr int kUnitSlots = 3;              // ring of tiles published to a CTA's roles
 
 // Arrive on another CTA's mbarrier without a release: for arrivals that order
@@ -56,15 +56,41 @@ __device__ __forceinline__ void arrive_relaxed_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-template <int EPI, int NMMA>
+// The instructions of one CTA (GROUP 1) or of a pair (GROUP 2).
+template <int GROUP>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  if constexpr (GROUP == 2) {
+    tma_load_2d_pair(dst, map, bar, c0, c1);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1) : "memory");
+  }
+}
+// Arrive on `bar` in each CTA of the group once the MMAs issued so far are done.
+template <int GROUP>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (GROUP == 2) umma_commit_pair_mc(bar, 0x3);
+  else umma_commit(bar);
+}
+template <int GROUP>
+__device__ __forceinline__ void group_sync() {
+  if constexpr (GROUP == 2) cluster_sync();
+  else __syncthreads();
+}
+
+template <int EPI, int NMMA, int GROUP>
 struct Cfg {
+  static constexpr int TILE_M = 128 * GROUP;
   static constexpr int NB = NMMA / 128;                  // scale tiles of B per 128 values of K
   static constexpr int OUT_N = EPI == EPI_SWIGLU ? NMMA / 2 : NMMA;
-  static constexpr int B_ROWS = NMMA / 2;                // B columns this CTA loads
+  static constexpr int B_ROWS = NMMA / GROUP;            // B columns this CTA loads
+  static constexpr int B_BOX = B_ROWS < 128 ? B_ROWS : 128;  // of one TMA box
   static constexpr int OPERANDS = kBoxBytes + B_ROWS * 128;
   static constexpr int SCALES = (1 + NB) * 2 * kScaleTile;
   static constexpr int STAGE_BYTES = OPERANDS + SCALES;  // a multiple of 1024
-  static constexpr int STAGES = NMMA == 256 ? 6 : 8;
+  static constexpr int STAGES = 224 * 1024 / STAGE_BYTES < 8 ? 224 * 1024 / STAGE_BYTES : 8;
   static constexpr int ACC1 = NMMA == 256 ? 224 : 128;   // first column of the second accumulator
   static constexpr int SF_COL = 480;
   static constexpr int TMEM_COLS = 512;
@@ -168,12 +194,12 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
   }
 }
 
-template <int EPI, int NMMA>
-__global__ void __launch_bounds__(Cfg<EPI, NMMA>::THREADS, 1)
+template <int EPI, int NMMA, int GROUP>
+__global__ void __launch_bounds__(Cfg<EPI, NMMA, GROUP>::THREADS, 1)
 grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmSA,
                   const __grid_constant__ CUtensorMap tmSB0, const __grid_constant__ CUtensorMap tmSB1, MxArgs args) {
-  using C = Cfg<EPI, NMMA>;
+  using C = Cfg<EPI, NMMA, GROUP>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES];
@@ -188,7 +214,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   __shared__ volatile int abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();  // 0: the CTA that issues the MMAs
+  const uint32_t rank = GROUP == 2 ? cluster_ctarank() : 0u;  // 0: the CTA that issues the MMAs
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
 
@@ -197,7 +223,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   if (threadIdx.x == 0) {
     abort_s = 0;
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], 2 * C::EPI_WARPS); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull_bar[b], 1); mbar_init(&tfree_bar[b], GROUP * C::EPI_WARPS); }
     for (int i = 0; i < kUnitSlots; ++i) {
       mbar_init(&unit_full[i], 1);
       mbar_init(&unit_empty[i], C::UNIT_READERS + (rank == 0 ? 1 : 0));
@@ -208,8 +234,13 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(&tmem_base_s, C::TMEM_COLS);
-    tmem_relinquish_pair();
+    if constexpr (GROUP == 2) {
+      tmem_alloc_pair(&tmem_base_s, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_base_s, C::TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   if (warp == C::SCHED_WARP && lane == 0) {
     prefetch_tmap(&tmA);
@@ -220,7 +251,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     prefetch_tmap(&tmSB1);
   }
   tc_fence_before();
-  cluster_sync();  // barriers initialised and tensor memory allocated in both CTAs
+  group_sync<GROUP>();  // barriers initialised and tensor memory allocated in every CTA of the group
   tc_fence_after();
   // The down projection follows the up projection, whose blocks all started
   // after the kernel before it was complete: its row segments can be read now,
@@ -234,12 +265,13 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     abort_s = 1;
   }
   constexpr uint32_t tmem_base = 0;
-  const int W = gridDim.x >> 1;     // pairs
+  const int W = gridDim.x / GROUP;  // groups
   const int katoms = args.K / 128;  // scale tiles along K
   const int nkb = (katoms + 1) / 2;
   // the even CTA's full and tfree barriers, as shared::cluster addresses
-  const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
-  const uint32_t tfree0 = mapa_shared(smem_u32(&tfree_bar[0]), 0);
+  // (GROUP 1: this CTA's)
+  const uint32_t full0 = GROUP == 2 ? mapa_shared(smem_u32(&full_bar[0]), 0) : smem_u32(&full_bar[0]);
+  const uint32_t tfree0 = GROUP == 2 ? mapa_shared(smem_u32(&tfree_bar[0]), 0) : smem_u32(&tfree_bar[0]);
 
   auto give_up = [&] {
     set_error(args.ctl, MOE_DEVERR_TIMEOUT);
@@ -265,16 +297,16 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   };
 
   if (warp == C::SCHED_WARP) {
-    TileList<kTileM> list;
+    TileList<C::TILE_M> list;
     load_segments(segments, args, lane, 32);
     __syncwarp();
     list.build(args, segments, args.N / C::OUT_N, lane);
-    const uint32_t pring1 = mapa_shared(smem_u32(&peer_ring[0]), 1);
-    const uint32_t pfull1 = mapa_shared(smem_u32(&peer_full[0]), 1);
-    const uint32_t pempty0 = mapa_shared(smem_u32(&peer_empty[0]), 0);
-    // Pair p starts with tile p, which both of its CTAs know; the counter hands
+    const uint32_t pring1 = GROUP == 2 ? mapa_shared(smem_u32(&peer_ring[0]), 1) : 0u;
+    const uint32_t pfull1 = GROUP == 2 ? mapa_shared(smem_u32(&peer_full[0]), 1) : 0u;
+    const uint32_t pempty0 = GROUP == 2 ? mapa_shared(smem_u32(&peer_empty[0]), 0) : 0u;
+    // Group g starts with tile g, which all of its CTAs know; the counter hands
     // out the tiles from W on.
-    int u = static_cast<int>(blockIdx.x >> 1);
+    int u = static_cast<int>(blockIdx.x) / GROUP;
     int slot = 0, pslot = 0;
     uint32_t phase = 0, pphase = 0;
     for (bool first = true;; first = false) {
@@ -298,7 +330,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         mbar_arrive(&unit_full[slot]);
       }
       if (rank == 0) {
-        if (!first) {
+        if (GROUP == 2 && !first) {
           // hand it over; the odd CTA frees the slot once it has taken it
           ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&peer_empty[pslot], pphase ^ 1u));
           if (!ok) {
@@ -313,7 +345,8 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             mbar_arrive_cluster(pfull1 + pslot * 8u);
           }
           if (++pslot == kUnitSlots) { pslot = 0; pphase ^= 1u; }
-        } else if (early) {
+        }
+        if (first && early) {
           pdl_begin();  // the counter is the previous kernel's until it is done
         }
         if (!end) {
@@ -349,20 +382,26 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       const int arow = t.row0 + 128 * static_cast<int>(rank);
       const int ga = (t.group + static_cast<int>(rank)) * katoms;
       const int gb = (t.e * ngroups + t.n0 / 128) * katoms;
-      // SwiGLU: CTA r loads matrix r's columns; otherwise CTA r its half
-      const CUtensorMap* mb = EPI == EPI_SWIGLU && rank == 1 ? &tmB1 : &tmB0;
-      const int brow = t.e * args.N + t.n0 + (EPI == EPI_SWIGLU ? 0 : C::B_ROWS * static_cast<int>(rank));
+      // SwiGLU: W_gate's columns, then W_up's; a pair's CTA r has the half r of
+      // all columns
+      const int brow = t.e * args.N + t.n0;
       auto load_weights = [&](int st, int kb) {
         uint8_t* sa = smem + st * C::STAGE_BYTES;
         uint8_t* ss = sa + C::OPERANDS;
         const uint32_t fb = full0 + st * 8u;
-        if (rank == 0) mbar_arrive_expect_tx(&full_bar[st], 2u * C::STAGE_BYTES);
-        tma_load_2d_pair(sa + kBoxBytes, mb, fb, kb * 128, brow);
+        if (rank == 0) mbar_arrive_expect_tx(&full_bar[st], GROUP * C::STAGE_BYTES);
+#pragma unroll
+        for (int j = 0; j < C::B_ROWS / C::B_BOX; ++j) {
+          const int col = C::B_ROWS * static_cast<int>(rank) + j * C::B_BOX;  // in the MMA's N
+          const bool up = EPI == EPI_SWIGLU && col >= C::OUT_N;
+          load_box<GROUP>(sa + kBoxBytes + j * C::B_BOX * 128, up ? &tmB1 : &tmB0, fb, kb * 128,
+                          brow + (up ? col - C::OUT_N : col));
+        }
         // two scale tiles each (the second is not used where K ends after one)
-        tma_load_2d_pair(ss + 2 * kScaleTile, &tmSB0, fb, 0, gb + 2 * kb);
+        load_box<GROUP>(ss + 2 * kScaleTile, &tmSB0, fb, 0, gb + 2 * kb);
         if (C::NB == 2)
-          tma_load_2d_pair(ss + 4 * kScaleTile, EPI == EPI_SWIGLU ? &tmSB1 : &tmSB0, fb, 0,
-                           (EPI == EPI_SWIGLU ? gb : gb + katoms) + 2 * kb);
+          load_box<GROUP>(ss + 4 * kScaleTile, EPI == EPI_SWIGLU ? &tmSB1 : &tmSB0, fb, 0,
+                          (EPI == EPI_SWIGLU ? gb : gb + katoms) + 2 * kb);
       };
       if (first) {
         ahead = min(STAGES, nkb);
@@ -380,8 +419,8 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         const uint32_t fb = full0 + stage * 8u;
         if (elect_one()) {
           if (kb >= ahead) load_weights(stage, kb);
-          tma_load_2d_pair(sa, &tmA, fb, kb * 128, arow);
-          tma_load_2d_pair(sa + C::OPERANDS, &tmSA, fb, 0, ga + 2 * kb);
+          load_box<GROUP>(sa, &tmA, fb, kb * 128, arow);
+          load_box<GROUP>(sa + C::OPERANDS, &tmSA, fb, 0, ga + 2 * kb);
         }
         __syncwarp();
         issued_mask |= 1u << stage;
@@ -399,8 +438,8 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   } else if (warp == 1) {
     if (early) pdl_begin();
     if (rank == 0) {
-      constexpr uint32_t kIdesc0 = make_idesc_mxf4(256, NMMA, 0);
-      constexpr uint32_t kIdesc2 = make_idesc_mxf4(256, NMMA, 2);
+      constexpr uint32_t kIdesc0 = make_idesc_mxf4(C::TILE_M, NMMA, 0);
+      constexpr uint32_t kIdesc2 = make_idesc_mxf4(C::TILE_M, NMMA, 2);
       const uint32_t base = smem_u32(smem);
       const uint64_t adesc0 = make_sw128_desc(base, 16, 1024);
       const uint64_t bdesc0 = make_sw128_desc(base + kBoxBytes, 16, 1024);
@@ -430,20 +469,20 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 if (at < atoms) {
                   const uint32_t sfa = tmem_base + C::SF_COL + (set ^ at) * 16;
                   const uint32_t sfb = sfa + 4;
-                  copy_scales<2>(sfa, sdesc0 + so + at * (kScaleTile >> 4));
+                  copy_scales<GROUP>(sfa, sdesc0 + so + at * (kScaleTile >> 4));
 #pragma unroll
                   for (int j = 0; j < C::NB; ++j)
-                    copy_scales<2>(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
+                    copy_scales<GROUP>(sfb + 4 * j, sdesc0 + so + ((1 + j) * 2 + at) * (kScaleTile >> 4));
 #pragma unroll
                   for (int kk = 0; kk < 2; ++kk) {
                     const uint32_t off = so + (at * 2 + kk) * 2;
-                    umma_mxf4<2>(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
+                    umma_mxf4<GROUP>(d_tmem, adesc0 + off, bdesc0 + off, kk == 0 ? kIdesc0 : kIdesc2, sfa, sfb,
                               (kb | at | kk) != 0 ? 1u : 0u);
                   }
                 }
               }
-              umma_commit_pair_mc(&empty_bar[stage], 0x3);
-              if (kb == nkb - 1) umma_commit_pair_mc(&tfull_bar[i & 1], 0x3);
+              commit<GROUP>(&empty_bar[stage]);
+              if (kb == nkb - 1) commit<GROUP>(&tfull_bar[i & 1]);
               issued_any = true;
             }
           }
@@ -458,7 +497,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       }
       if (__any_sync(0xffffffffu, issued_any)) {
         // Tensor memory is freed below: wait until every MMA issued is done.
-        if (elect_one()) umma_commit_pair_mc(&drain_bar, 0x1);
+        if (elect_one()) {
+          if constexpr (GROUP == 2) umma_commit_pair_mc(&drain_bar, 0x1);
+          else umma_commit(&drain_bar);
+        }
         __syncwarp();
         (void)mbar_wait_bounded(&drain_bar, 0);
       }
@@ -480,7 +522,10 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       auto free_overlap = [&] {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_relaxed_cluster(tfree0 + acc * 8u);
+        if (lane == 0) {
+          if constexpr (GROUP == 2) arrive_relaxed_cluster(tfree0 + acc * 8u);
+          else mbar_arrive(&tfree_bar[acc]);
+        }
       };
       const int crow = 128 * static_cast<int>(rank) + q * 32;
       // The shared columns are in the last group of the first accumulator
@@ -494,31 +539,51 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no peer still reads or signals this CTA; every MMA is done
+  group_sync<GROUP>();  // no peer still reads or signals this CTA; every MMA is done
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem_base_s, C::TMEM_COLS);
+    if constexpr (GROUP == 2) tmem_dealloc_pair(tmem_base_s, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base_s, C::TMEM_COLS);
   }
 }
 
-template <int EPI, int NMMA>
-cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
-  using C = Cfg<EPI, NMMA>;
+template <int EPI, int NMMA, int GROUP>
+cudaError_t run_group(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
+  using C = Cfg<EPI, NMMA, GROUP>;
   CUtensorMap ta, tb0, tb1, sa, sb0, sb1;
   const uint64_t brows = static_cast<uint64_t>(args.E) * args.N, katoms = args.K / 128;
   const uint64_t atiles = (static_cast<uint64_t>(args.rows_max) / 128 + args.E) * katoms;
   const MxWeights& up = EPI == EPI_SWIGLU ? b1 : b0;
   if (!make_tma_codes(&ta, a.codes, static_cast<uint64_t>(args.rows_max), args.K / 2, 128) ||
-      !make_tma_codes(&tb0, b0.codes, brows, args.K / 2, C::B_ROWS) ||
-      !make_tma_codes(&tb1, up.codes, brows, args.K / 2, C::B_ROWS) ||
+      !make_tma_codes(&tb0, b0.codes, brows, args.K / 2, C::B_BOX) ||
+      !make_tma_codes(&tb1, up.codes, brows, args.K / 2, C::B_BOX) ||
       !make_tma_scales(&sa, a.scales, atiles) || !make_tma_scales(&sb0, b0.scales, brows / 128 * katoms) ||
       !make_tma_scales(&sb1, up.scales, brows / 128 * katoms))
     return cudaErrorInvalidValue;
-  auto kern = grouped_gemm_mxf4<EPI, NMMA>;
+  auto kern = grouped_gemm_mxf4<EPI, NMMA, GROUP>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
-  const int pairs = num_sms() / 2;
-  return launch_pdl_cluster(kern, dim3(2 * pairs), dim3(C::THREADS), C::SMEM, s, 2, ta, tb0, tb1, sa, sb0, sb1, args);
+  const int grid = num_sms() / GROUP * GROUP;
+  if constexpr (GROUP == 2)
+    return launch_pdl_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, s, 2, ta, tb0, tb1, sa, sb0, sb1, args);
+  else
+    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, s, false, ta, tb0, tb1, sa, sb0, sb1, args);
 }
+
+template <int EPI, int NMMA>
+cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, bool pairs,
+                     cudaStream_t s) {
+  return pairs ? run_group<EPI, NMMA, 2>(a, b0, b1, args, s) : run_group<EPI, NMMA, 1>(a, b0, b1, args, s);
+}
+
+// Experts of at least this many rows on average (of rows_max, which is all the
+// host knows) run on CTA pairs, others on single CTAs, whose 128-row tiles fill
+// better. Measured, single against pairs: Mixtral-shaped (8 experts, d 4096, F
+// 14336) 64 rows an expert 130 / 152 us, 128 rows 164 / 157, 256 rows 232 / 222,
+// 512 rows 372 / 346, 1024 rows 659 / 570; 64 experts (d 1024, F 4096, GELU) 128
+// rows 80 / 88, 512 rows 175 / 163; 64 skewed experts (d 4096, F 2048) 128 rows
+// 181 / 207. Where a capacity drops much of rows_max the bound misleads (512 of
+// bound, 173 of rows: 90 / 100).
+constexpr int64_t kPairRows = 256;
 
 }  // namespace
 
@@ -551,22 +616,23 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
     if (after_up) cudaEventRecord(after_up, s);
     return err;
   }
+  const bool pairs = rows_max >= kPairRows * E;
   a.K = d;
   a.N = F;
   cudaError_t err;
   if (act == MOE_ACT_SWIGLU)
-    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
+    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, pairs, s);
   else if (F % 256 == 0)
-    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
+    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, pairs, s);
   else
-    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, s);
+    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, pairs, s);
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
   a.early = 1;
   a.K = F;
   a.N = d;
-  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
-  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
+  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, pairs, s);
+  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, pairs, s);
 }
 
 }  // namespace moe
