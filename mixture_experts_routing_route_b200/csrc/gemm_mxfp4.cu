@@ -9,17 +9,19 @@
 //      scales of h); or the plain bf16 store of the down projection. Sums and
 //      activations are fp32; h is rounded once (to E2M1), y once (to bf16).
 //
-// Two forms of one kernel. GROUP 2, for experts with many rows: the two CTAs of
-// a cluster compute one 256-row x N tile together (cta_group::2). GROUP 1: a CTA
-// computes a 128-row x N tile. Both are persistent. As a pair, CTA r holds A rows [row0 + 128 r, +128) and its
-// half of the B columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output
-// columns), its rows' scales and the scales of all B columns. Its warps:
+// Two forms of one kernel, both persistent. GROUP 2, for experts with many rows
+// and long K: the two CTAs of a cluster compute one 256-row x N tile together
+// (cta_group::2); CTA r holds A rows [row0 + 128 r, +128) and its half of the B
+// columns (SwiGLU: CTA 0 W_gate's, CTA 1 W_up's of the same output columns), its
+// rows' scales and the scales of all B columns. GROUP 1: a CTA computes a
+// 128-row x N tile and holds all B columns. A CTA's warps:
 //   warp 0   producer: per stage (256 values of K) the A and B boxes by TMA (128
 //            bytes = 256 codes a row, 128-byte swizzle) and the scale tiles (two
 //            of 512 bytes per 128 rows)
-//   warp 1   MMA issuer (of a pair: the even CTA's): per 128 values of K one thread copies the
-//            scale tiles to tensor memory of both CTAs (tcgen05.cp, replicated
-//            to the four lane quarters) and issues two MMAs of K = 64
+//   warp 1   MMA issuer (of a pair: the even CTA's): per 128 values of K one
+//            thread copies the scale tiles to tensor memory (of both CTAs;
+//            tcgen05.cp, replicated to the four lane quarters) and issues two
+//            MMAs of K = 64
 //   8 or 16  epilogue: a thread per row and a half or a quarter of the columns,
 //            32 columns (one block) at a time
 //   the last scheduler: hands out tiles
@@ -35,12 +37,13 @@
 //
 // Work is handed out dynamically, as in the bf16 CTA-pair kernel, so that CTAs
 // sharing a weight block read it at nearly the same time: the even CTA's
-// scheduler (GROUP 1: each CTA's) takes the next tile from a counter in the control block, decodes
-// it, publishes it to its CTA's roles and hands it to the odd CTA's scheduler,
-// if there is one, which does the same there. The three-slot ring keeps this chain (some 3000
-// cycles a tile: the counter, a search with a division, waits and releases at
-// cluster scope) off every other role's path, and takes no tile so early that
-// a slow pair would hold work an idle one could do.
+// scheduler (GROUP 1: each CTA's) takes the next tile from a counter in the
+// control block, decodes it, publishes it to its CTA's roles and hands it to the
+// odd CTA's scheduler, if there is one, which does the same there. The
+// three-slot ring keeps this chain (some 3000 cycles a tile of a pair: the
+// counter, a search with a division, waits and releases at cluster scope) off
+// every other role's path, and takes no tile so early that a slow pair would
+// hold work an idle one could do.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
 #include "mxfp4_gemm.cuh"
 
@@ -569,21 +572,24 @@ cudaError_t run_group(const MxRows& a, const MxWeights& b0, const MxWeights& b1,
     return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, s, false, ta, tb0, tb1, sa, sb0, sb1, args);
 }
 
-template <int EPI, int NMMA>
-cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, bool pairs,
-                     cudaStream_t s) {
-  return pairs ? run_group<EPI, NMMA, 2>(a, b0, b1, args, s) : run_group<EPI, NMMA, 1>(a, b0, b1, args, s);
-}
-
-// Experts of at least this many rows on average (of rows_max, which is all the
-// host knows) run on CTA pairs, others on single CTAs, whose 128-row tiles fill
-// better. Measured, single against pairs: Mixtral-shaped (8 experts, d 4096, F
-// 14336) 64 rows an expert 130 / 152 us, 128 rows 164 / 157, 256 rows 232 / 222,
-// 512 rows 372 / 346, 1024 rows 659 / 570; 64 experts (d 1024, F 4096, GELU) 128
-// rows 80 / 88, 512 rows 175 / 163; 64 skewed experts (d 4096, F 2048) 128 rows
-// 181 / 207. Where a capacity drops much of rows_max the bound misleads (512 of
-// bound, 173 of rows: 90 / 100).
+// A product runs on CTA pairs where experts have many rows on average (of
+// rows_max, which is all the host knows) and K is long; single CTAs' 128-row
+// tiles fill better, and with short K a tile's turnaround counts, which the
+// second CTA lengthens. Measured, whole FFN, single against pairs for both
+// products: 8 experts, d 4096, F 14336: 32 rows an expert 131 / 154 us, 128 rows
+// 166 / 159, 256 rows 229 / 220, 512 rows 377 / 350, 1024 rows 659 / 570; 64
+// experts, d 4096, F 2048, skewed, 128 rows 182 / 208, 512 rows 469 / 457; d
+// 2048, F 1408: 256 rows 116 / 115, 512 rows 189 / 181. With d 1024, F 4096, 512
+// rows: singles 195, pairs for the down projection alone 191, for both 195; if a
+// capacity leaves 173 of the 512: 91, 92, 102.
 constexpr int64_t kPairRows = 256;
+constexpr int kPairK = 2048;
+
+template <int EPI, int NMMA>
+cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
+  if (args.rows_max >= kPairRows * args.E && args.K >= kPairK) return run_group<EPI, NMMA, 2>(a, b0, b1, args, s);
+  return run_group<EPI, NMMA, 1>(a, b0, b1, args, s);
+}
 
 }  // namespace
 
@@ -616,23 +622,22 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
     if (after_up) cudaEventRecord(after_up, s);
     return err;
   }
-  const bool pairs = rows_max >= kPairRows * E;
   a.K = d;
   a.N = F;
   cudaError_t err;
   if (act == MOE_ACT_SWIGLU)
-    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, pairs, s);
+    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
   else if (F % 256 == 0)
-    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, pairs, s);
+    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
   else
-    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, pairs, s);
+    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, s);
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
   a.early = 1;
   a.K = F;
   a.N = d;
-  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, pairs, s);
-  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, pairs, s);
+  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
+  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
 }
 
 }  // namespace moe
