@@ -135,6 +135,27 @@ __device__ __forceinline__ uint32_t quantise_block(float (&h)[32], uint4& codes)
   return sb;
 }
 
+// Among four neighbouring lanes, p[i] of lane j becomes p[j] of lane i.
+__device__ __forceinline__ void transpose_quad(uint4 (&p)[4], int lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d *= 2) {
+    const bool hi = lane & d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & d) continue;
+      uint4& a = p[i];
+      uint4& b = p[i + d];
+      uint4 g = hi ? a : b;  // given away
+      g.x = __shfl_xor_sync(0xffffffffu, g.x, d);
+      g.y = __shfl_xor_sync(0xffffffffu, g.y, d);
+      g.z = __shfl_xor_sync(0xffffffffu, g.z, d);
+      g.w = __shfl_xor_sync(0xffffffffu, g.w, d);
+      if (hi) a = g;
+      else b = g;
+    }
+  }
+}
+
 // One warp's 32 rows (crow: the first in the tile) and the column groups [g0,
 // g0 + G) of 32. reverse: the last group first; `free_overlap` is called once
 // the first group's loads are done.
@@ -172,13 +193,17 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
     }
     const int col = t.n0 + 32 * g;
     if constexpr (EPI == EPI_STORE) {
-      if (valid) {
-        uint4* dst = reinterpret_cast<uint4*>(args.out + row * args.N + col);
+      uint4 p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack_bf16(h[8 * i], h[8 * i + 1]), pack_bf16(h[8 * i + 2], h[8 * i + 3]),
-                              pack_bf16(h[8 * i + 4], h[8 * i + 5]), pack_bf16(h[8 * i + 6], h[8 * i + 7]));
-      }
+      for (int i = 0; i < 4; ++i)
+        p[i] = make_uint4(pack_bf16(h[8 * i], h[8 * i + 1]), pack_bf16(h[8 * i + 2], h[8 * i + 3]),
+                          pack_bf16(h[8 * i + 4], h[8 * i + 5]), pack_bf16(h[8 * i + 6], h[8 * i + 7]));
+      transpose_quad(p, lane);
+      const int quad = crow + (lane & ~3);
+      __nv_bfloat16* dst = args.out + (static_cast<size_t>(t.row0) + quad) * args.N + col + 8 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (quad + i < t.rows) *reinterpret_cast<uint4*>(dst + static_cast<size_t>(i) * args.N) = p[i];
     } else {
       uint4 codes;
       const uint32_t sb = quantise_block(h, codes);
