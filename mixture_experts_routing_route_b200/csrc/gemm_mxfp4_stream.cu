@@ -3,15 +3,15 @@
 //
 // Nothing is reused there: the weights of the chosen experts are read once and
 // that is the time. One kernel streams them, up projection, then down
-// projection, with tensor cores in the stream. Against the CTA-pair kernel
-// (gemm_mxfp4.cu):
+// projection, with tensor cores in the stream. Against the tiles of
+// gemm_mxfp4.cu:
 //  - the operands change places: 128 weight rows (output columns) are the M
 //    side, up to 32 tokens the N side, so an MMA costs a tenth and a tile of
-//    one token wastes no operand loads (a pair's tile costs 512 cycles of MMA
-//    per stage whatever its rows, 69 GB/s of weights an SM);
+//    one token wastes no operand loads (a tile there costs 512 cycles of MMA per
+//    stage whatever its rows, 69 GB/s of weights an SM);
 //  - every SM gets the same number of stages (128 weight rows x 256 or 512
-//    values of K) of each projection: the stages of all tiles in one line, cut into as
-//    many equal ranges as there are blocks. A tile cut between ranges is
+//    values of K) of each projection: the stages of all tiles in one line, cut
+//    into as many equal ranges as there are blocks. A tile cut between ranges is
 //    finished by the block that comes to it last, which adds the pieces in the
 //    order of K (the same order whoever is last: the same bits);
 //  - both projections are one launch. The down projection's first weights are
