@@ -612,7 +612,9 @@ MOE_API moe_status_t moe_expert_ffn_mxfp4(const void* x_codes, const void* x_sca
  * no work.
  *   x [T, d], out [T, d] (dtype); aux_loss out [1] fp32 device or NULL.
  *   events: NULL, or 7 cudaEvent_t recorded on `stream` before route and
- *   after route, permute, gather, up-projection, down-projection, combine.
+ *   after route, permute, gather, up-projection, down-projection, combine. With
+ *   MOE_LAYER_MXFP4 and at most 32 rows both projections are one launch and
+ *   the "up-projection" event follows it.
  *   ws >= moe_forward_workspace_size(layer, T) bytes; it holds every
  *   intermediate (see moe_forward_views). */
 MOE_API size_t moe_forward_workspace_size(const moe_layer_t* layer, int T);

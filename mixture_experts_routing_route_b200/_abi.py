@@ -7,6 +7,7 @@ if the library is missing or cannot load, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -415,9 +416,13 @@ def layer_struct(d, E, k, F, dtype, act, cf, w_router, bias, w1, w3, w2, flags=0
 def quantize_expert_weights(w: torch.Tensor, stream=None):
     """Expert weights [E, K, N] (bf16 or fp32, on the GPU) as MXFP4: codes [E, N, K / 2] and scales."""
     E, K, N = w.shape
-    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(moe_mxfp4_weight_scales_size(E, K, N), dtype=torch.uint8, device=w.device)
-    moe_mxfp4_quantize_weights(w.contiguous(), E, K, N, codes, scales, stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    # the copy and the allocations too belong to the stream that the kernel runs on
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(moe_mxfp4_weight_scales_size(E, K, N), dtype=torch.uint8, device=w.device)
+        moe_mxfp4_quantize_weights(w.contiguous(), E, K, N, codes, scales, stream)
     return codes, scales
 
 

@@ -34,13 +34,15 @@ class MoeLayer:
         # and only their codes and scales are kept. x and out are bf16.
         self.mxfp4 = mxfp4
         if mxfp4:
+            if w_router.dtype != torch.bfloat16:
+                raise ValueError("w_router must be bf16 with mxfp4 experts")
             self.dtype = torch.bfloat16
             self.w1, s1 = abi.quantize_expert_weights(w1)
             self.w3, s3 = (None, None) if w3 is None else abi.quantize_expert_weights(w3)
             self.w2, s2 = abi.quantize_expert_weights(w2)
             self.scales = (s1, s3, s2)
-            if w_router.dtype != torch.bfloat16:
-                raise ValueError("w_router must be bf16 with mxfp4 experts")
+            # forward may be called on any stream
+            torch.cuda.current_stream().synchronize()
         else:
             self.w1 = w1.contiguous()
             self.w3 = None if w3 is None else w3.contiguous()

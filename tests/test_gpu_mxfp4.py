@@ -96,7 +96,7 @@ def test_nearest_code_of_every_bf16_magnitude():
 
 ROWS = [
     (1, 128, 1, 1, "bf16", 0.0),
-    (1, 4096, 8, 2, "bf16", 0.0),
+    (1, 4096, 8, 2, "bf16", 0.0),         # (binned: a capacity of no row)
     (130, 384, 4, 2, "f32", 1.0),
     (77, 1152, 16, 8, "bf16", 0.0),       # a row of one chunk and a bit
     (1000, 256, 256, 3, "f32", 0.5),
@@ -108,8 +108,6 @@ ROWS = [
 @pytest.mark.parametrize("binned", [False, True])
 def test_gather(T, d, E, k, dt, cf, binned):
     _, _, p, rows = routing(T, E, k, cf if not binned else max(cf, 1.0), T + d, binned)
-    if rows == 0:
-        pytest.skip("capacity of no row")
     x = awkward((T, d), dt, T).to(DEV)
     codes, scales = u8(rows * d // 2), u8(abi.moe_mxfp4_row_scales_size(rows, E, d))
     out = torch.full((rows, d), 77.0, dtype=DT[dt], device=DEV)
@@ -130,6 +128,29 @@ def test_gather(T, d, E, k, dt, cf, binned):
     got = np32(out).astype(np.float64)
     assert np.array_equal(got[row], R.values(rc, rs)[token], equal_nan=True)
     assert np.all(got[seg[E]:] == 77.0)
+
+
+def test_weights_are_quantised_on_the_stream_given():
+    """A transposed matrix has to be copied first: on the same stream, behind
+    what fills it there."""
+    side = torch.cuda.Stream()
+    wt = awkward((2, 512, 256), "bf16", 3).to(DEV)
+    rc, rs = R.quantise(wt.float().cpu().numpy())
+    w = torch.zeros_like(wt)
+    abi.quantize_expert_weights(w.transpose(1, 2))  # loads every kernel (a first launch waits for the device)
+    with torch.cuda.stream(side):
+        w.copy_(wt)
+    for stream in (side, side.cuda_stream):
+        w.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+            w.copy_(wt)
+        codes, scales = abi.quantize_expert_weights(w.transpose(1, 2), stream)
+        torch.full_like(w, 9.0)  # may take memory that the current stream freed
+        torch.cuda.synchronize()
+        assert np.array_equal(R.unpack(npi(codes).reshape(2, 512, 128)), rc)
+        assert np.array_equal(R.weight_scales(npi(scales), 2, 256, 512), rs)
 
 
 def test_gather_reports_rows_out_of_range():
@@ -253,6 +274,20 @@ FFN = [
 ]
 
 
+# 256 rows an expert or more (of the buffer) and K >= 2048: CTA pairs
+PAIRS = [
+    # E, d, F, counts, act, rows past the last
+    (2, 2048, 384, [33, 700], "swiglu", 0),        # up; single CTAs down
+    (2, 2176, 2304, [511, 1], "swiglu", 0),        # both; half stages, N = 128 tiles down
+    (1, 2048, 2304, [256], "gelu", 0),             # a whole tile
+    (1, 2304, 2176, [257], "gelu", 3),             # one row more; N = 128 tiles up
+    (3, 384, 4096, [0, 300, 500], "gelu", 0),      # down; single CTAs up
+    (4, 4096, 2048, [1, 0, 1000, 130], "swiglu", 0),
+    (8, 2048, 2048, [5, 0, 0, 0, 130, 0, 0, 1], "swiglu", 2048),  # few rows of a large buffer
+    (3, 2048, 2048, [0, 0, 0], "gelu", 900),       # none
+]
+
+
 # a decode step: at most 32 rows in all (the weight stream, tiles cut between blocks)
 FEW = [
     (1, 128, 128, [1], "swiglu"),
@@ -276,6 +311,11 @@ def test_ffn(E, d, F, counts, act, extra):
     check_ffn(ex, rows, seg, xc, xs, hc, hs, y)
 
 
+@pytest.mark.parametrize("E,d,F,counts,act,extra", PAIRS)
+def test_ffn_pairs(E, d, F, counts, act, extra):
+    test_ffn(E, d, F, counts, act, extra)
+
+
 def test_ffn_no_rows_in_use():
     ex = Experts(4, 128, 256, "swiglu", 1)
     rows, seg, xc, xs = rows_of(ex, [0, 0, 0, 0], 8, 1)
@@ -284,19 +324,23 @@ def test_ffn_no_rows_in_use():
     assert torch.all(y == 77.0) and torch.all(hc == 255)
 
 
-def test_ffn_nan_rows_stay_alone():
-    ex = Experts(2, 256, 256, "swiglu", 2)
-    rows, seg, xc, xs = rows_of(ex, [40, 50], 0, 3)
+@pytest.mark.parametrize("d,counts", [(256, [40, 50]), (2048, [40, 500]), (256, [4, 60]), (256, [20, 12])])
+def test_ffn_nan_rows_stay_alone(d, counts):
+    ex = Experts(2, d, d, "swiglu", 2)
+    rows, seg, xc, xs = rows_of(ex, counts, 0, 3)
+    bad_row = rows - 5
     g, r = R.row_groups(npi(seg))
-    xs[int(R.scale_at(g[45], 2, r[45], 1))] = 255   # one NaN block
+    xs[int(R.scale_at(g[bad_row], d // 128, r[bad_row], 1))] = 255   # one NaN block
     _, _, y, ws = run_ffn(ex, xc, xs, rows, seg)
     bad = torch.isnan(y).any(1)
-    assert bad.sum().item() == 1 and bad[45].item() and torch.isnan(y[45]).all()
+    assert bad.sum().item() == 1 and bad[bad_row].item() and torch.isnan(y[bad_row]).all()
 
 
-@pytest.mark.parametrize("counts", [[130, 0, 4, 260, 1, 70], [3, 0, 4, 0, 1, 17]])
-def test_ffn_repeats_bit_for_bit_on_one_workspace_and_in_a_graph(counts):
-    ex = Experts(6, 512, 1024, "swiglu", 4)
+@pytest.mark.parametrize("d,F,counts", [(512, 1024, [130, 0, 4, 260, 1, 70]), (512, 1024, [3, 0, 4, 0, 1, 17]),
+                                        (2048, 2048, [900, 0, 300, 1, 257, 100]),
+                                        (512, 2048, [900, 0, 300, 1, 257, 100])])
+def test_ffn_repeats_bit_for_bit_on_one_workspace_and_in_a_graph(d, F, counts):
+    ex = Experts(6, d, F, "swiglu", 4)
     rows, seg, xc, xs = rows_of(ex, counts, 3, 5)
     hc, hs, y, ws = run_ffn(ex, xc, xs, rows, seg)
     for _ in range(3):

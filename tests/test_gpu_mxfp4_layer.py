@@ -53,6 +53,8 @@ CASES = [
     (300, 384, 8, 2, 640, "gelu", 1.0, False),      # drops
     (700, 256, 5, 3, 512, "swiglu", 0.0, False),
     (257, 512, 64, 4, 256, "swiglu", 1.25, True),
+    (1100, 2048, 2, 2, 512, "swiglu", 0.0, False),  # CTA pairs up, single CTAs down
+    (600, 2048, 4, 2, 2048, "gelu", 2.0, True),     # CTA pairs, bins partly full
 ]
 
 
