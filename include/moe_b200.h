@@ -192,7 +192,8 @@ MOE_API moe_status_t moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t 
 
 /* Set how long a kernel using this workspace waits at a barrier between its
  * CTAs (the permute's grid barrier, where every CTA waits for all others to
- * publish their counts) before it gives up: it then sets MOE_DEVERR_TIMEOUT,
+ * publish their counts; in moe_expert_ffn_mxfp4 with at most 32 rows the down
+ * projection's wait for h) before it gives up: it then sets MOE_DEVERR_TIMEOUT,
  * skips the work that needed the barrier and returns, leaving the GPU
  * context usable. limit_us in microseconds; 0 restores the default of 2 s.
  * Written asynchronously on `stream` (one small kernel). The waits inside a

@@ -25,9 +25,10 @@
 //   8 or 16  epilogue: a thread per row and a half or a quarter of the columns,
 //            32 columns (one block) at a time
 //   the last scheduler: hands out tiles
-// Why pairs: a 128 x 256 tile of one CTA needs 51 KB from L2 per 512 clocks of
-// MMA, 100 bytes per clock and SM; a pair's CTA needs 35 KB, which it gets: a
-// stage takes 525 to 540 clocks (K = 4096 and 14336).
+// Why pairs: a stage of a 128 x 256 tile is 51 KB that come from L2 and go
+// through one CTA's shared memory twice (written, read by the MMAs), some 790
+// clocks at 128 bytes a clock for 512 clocks of MMA (measured: 800). A pair's CTA
+// has 35 KB a stage for the same MMA time: 525 to 540 clocks (K = 4096 and 14336).
 //
 // Tensor memory: two accumulators of 256 columns and the scales do not fit in
 // 512 columns, so the accumulators overlap by 32 columns (columns 0-255 and
@@ -97,10 +98,10 @@ struct Cfg {
   static constexpr int ACC1 = NMMA == 256 ? 224 : 128;   // first column of the second accumulator
   static constexpr int SF_COL = 480;
   static constexpr int TMEM_COLS = 512;
-  // epilogue warps: four lane quarters x PARTS of the columns. GELU: the
-  // activation bounds short K, and four warps a scheduler hide its latencies
-  // (capacity workload 106 -> 102 us); elsewhere they cost (Mixtral-shaped 574
-  // -> 601 us: more warps waiting on shared memory beside the MMAs).
+  // epilogue warps: four lane quarters x PARTS of the columns. GELU: four warps
+  // a scheduler hide the activation's latencies (d 1024, 64 experts of 128 rows
+  // 78 -> 75 us); elsewhere they cost (Mixtral-shaped 574 -> 601 us: more warps
+  // waiting on shared memory beside the MMAs).
   static constexpr int PARTS = EPI == EPI_GELU ? 4 : 2;
   static constexpr int EPI_WARPS = 4 * PARTS;
   static constexpr int SCHED_WARP = 2 + EPI_WARPS;
@@ -563,7 +564,7 @@ grouped_gemm_mxf4(const __grid_constant__ CUtensorMap tmA, const __grid_constant
       // The shared columns are in the last group of the first accumulator
       // (last part's warps) and in the first group of the second. A warp
       // without rows leaves the others its issue slots (a skewed layer's last
-      // tiles have few rows: capacity workload 108 -> 106 us).
+      // tiles have few rows: 2% there).
       if (crow >= t.rows) free_overlap();
       else epilogue<EPI, C::OUT_N, G>(tbase, args, t, crow, lane, part * G, acc == 0,
                                  free_overlap);

@@ -383,6 +383,30 @@ def test_ffn_bad_segments_set_the_error_bit():
     assert torch.all(y[10:] == 77.0)  # the bad expert's rows are skipped
 
 
+def test_decode_wait_for_h_runs_out_then_workspace_init_recovers():
+    """The down projection's blocks of a decode step wait until the up
+    projection's ranges are done, at most the workspace's wait limit. Here the
+    counter that hands out the ranges starts behind those of the up projection,
+    so nobody does them: every block gives up after 1 ms, sets
+    MOE_DEVERR_TIMEOUT and returns, and the context stays usable."""
+    stream_next = 188  # byte of that counter in the control block
+    ex = Experts(8, 4096, 1792, "swiglu", 11)
+    rows, seg, xc, xs = rows_of(ex, [0, 1, 0, 0, 0, 0, 1, 0], 0, 12)  # 448 stages up, 256 down
+    hc, hs, y, ws = run_ffn(ex, xc, xs, rows, seg)
+    abi.moe_workspace_set_wait_limit(ws, 1000)
+    again = run_ffn(ex, xc, xs, rows, seg, ws=ws)  # the limit alone changes nothing
+    assert torch.equal(again[2], y) and abi.moe_get_device_error(ws) == 0
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws[stream_next:stream_next + 4].view(torch.int32).fill_(sms)  # a range each of the up projection
+    run_ffn(ex, xc, xs, rows, seg, ws=ws)
+    torch.cuda.synchronize()
+    assert abi.moe_get_device_error(ws) & abi.DEVERR_TIMEOUT
+    abi.moe_workspace_init(ws)
+    again = run_ffn(ex, xc, xs, rows, seg, ws=ws)
+    assert abi.moe_get_device_error(ws) == 0
+    assert torch.equal(again[0], hc) and torch.equal(again[2], y)
+
+
 def test_quantise_gather_ffn_combine_together():
     """The operators one after another as a layer uses them: routing and permute
     of this library, 4-bit gather and experts, the bf16 combine."""
