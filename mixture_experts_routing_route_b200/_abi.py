@@ -169,20 +169,25 @@ def _stream(stream) -> int:
 
 
 def _on_gpu(*tensors):
-    """Refuse what would fault or be misread on the GPU: a tensor that is not on
-    the current device (its kernels and streams are the current device's), or
-    not contiguous."""
+    """The addresses of tensors (None: NULL). Refuses what would fault or be
+    misread on the GPU: a tensor that is not on the current device (its kernels
+    and streams are the current device's), or not contiguous."""
     current = None
+    out = []
     for t in tensors:
         if t is None:
+            out.append(None)
             continue
         d = t.get_device()
-        if d >= 0 and current is None:
-            current = torch.cuda.current_device() if _current_device is None else _current_device()
-        if d < 0 or d != current:
-            raise ValueError(f"tensor on {t.device}, not on the current CUDA device")
+        if d != current:
+            if current is None and d >= 0:
+                current = torch.cuda.current_device() if _current_device is None else _current_device()
+            if d != current:
+                raise ValueError(f"tensor on {t.device}, not on the current CUDA device")
         if not t.is_contiguous():
             raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
+        out.append(t.data_ptr())
+    return out
 
 
 def _check(fn: str, st: int):
@@ -330,17 +335,17 @@ def moe_combine(y_perm, topk_w, slot_to_row, T, d, k, rows_max, out, ws, stream=
 
 def moe_combine_backward(d_out, y_perm, topk_w, slot_to_row, T, d, k, rows_max, d_y_perm, d_topk_w,
                          ws, stream=None):
-    _on_gpu(d_out, y_perm, topk_w, slot_to_row, d_y_perm, d_topk_w, ws)
+    g, y, w, s2r, dy, dw, wsp = _on_gpu(d_out, y_perm, topk_w, slot_to_row, d_y_perm, d_topk_w, ws)
     _check("moe_combine_backward", _lib.moe_combine_backward(
-        _ptr(d_out), _ptr(y_perm), _ptr(topk_w), _ptr(slot_to_row), dtype_code(d_out.dtype), T, d,
-        k, int(rows_max), _ptr(d_y_perm), _ptr(d_topk_w), _ptr(ws), ws.numel(), _stream(stream)))
+        g, y, w, s2r, dtype_code(d_out.dtype), T, d, k, int(rows_max), dy, dw, wsp, ws.numel(),
+        _stream(stream)))
 
 
 def moe_gather_backward(d_x_perm, slot_to_row, dx_in, T, d, k, rows_max, dx, ws, stream=None):
-    _on_gpu(d_x_perm, slot_to_row, dx_in, dx, ws)
+    g, s2r, add, out, wsp = _on_gpu(d_x_perm, slot_to_row, dx_in, dx, ws)
     _check("moe_gather_backward", _lib.moe_gather_backward(
-        _ptr(d_x_perm), _ptr(slot_to_row), _ptr(dx_in), dtype_code(dx.dtype), T, d, k,
-        int(rows_max), _ptr(dx), _ptr(ws), ws.numel(), _stream(stream)))
+        g, s2r, add, dtype_code(dx.dtype), T, d, k, int(rows_max), out, wsp, ws.numel(),
+        _stream(stream)))
 
 
 def moe_mxfp4_weight_scales_size(E: int, K: int, N: int) -> int:
@@ -352,30 +357,30 @@ def moe_mxfp4_row_scales_size(rows_max: int, E: int, K: int) -> int:
 
 
 def moe_mxfp4_quantize_weights(w, E, K, N, codes, scales, stream=None):
-    _on_gpu(w, codes, scales)
+    wp, c, sc = _on_gpu(w, codes, scales)
     _check("moe_mxfp4_quantize_weights", _lib.moe_mxfp4_quantize_weights(
-        _ptr(w), dtype_code(w.dtype), E, K, N, _ptr(codes), _ptr(scales), _stream(stream)))
+        wp, dtype_code(w.dtype), E, K, N, c, sc, _stream(stream)))
 
 
 def moe_mxfp4_dequantize_weights(codes, scales, E, K, N, w, stream=None):
-    _on_gpu(codes, scales, w)
+    c, sc, wp = _on_gpu(codes, scales, w)
     _check("moe_mxfp4_dequantize_weights", _lib.moe_mxfp4_dequantize_weights(
-        _ptr(codes), _ptr(scales), dtype_code(w.dtype), E, K, N, _ptr(w), _stream(stream)))
+        c, sc, dtype_code(w.dtype), E, K, N, wp, _stream(stream)))
 
 
 def moe_gather_mxfp4(x, T, d, k, slot_to_row, seg_offsets, E, rows_max, codes, scales, ws,
                      stream=None):
-    _on_gpu(x, slot_to_row, seg_offsets, codes, scales, ws)
+    xp, s2r, seg, c, sc, wsp = _on_gpu(x, slot_to_row, seg_offsets, codes, scales, ws)
     _check("moe_gather_mxfp4", _lib.moe_gather_mxfp4(
-        _ptr(x), dtype_code(x.dtype), T, d, k, _ptr(slot_to_row), _ptr(seg_offsets), E,
-        int(rows_max), _ptr(codes), _ptr(scales), _ptr(ws), ws.numel(), _stream(stream)))
+        xp, dtype_code(x.dtype), T, d, k, s2r, seg, E, int(rows_max), c, sc, wsp, ws.numel(),
+        _stream(stream)))
 
 
 def moe_mxfp4_dequantize_rows(codes, scales, seg_offsets, E, rows_max, K, out, ws, stream=None):
-    _on_gpu(codes, scales, seg_offsets, out, ws)
+    c, sc, seg, o, wsp = _on_gpu(codes, scales, seg_offsets, out, ws)
     _check("moe_mxfp4_dequantize_rows", _lib.moe_mxfp4_dequantize_rows(
-        _ptr(codes), _ptr(scales), _ptr(seg_offsets), E, int(rows_max), K, dtype_code(out.dtype),
-        _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+        c, sc, seg, E, int(rows_max), K, dtype_code(out.dtype), o, wsp, ws.numel(),
+        _stream(stream)))
 
 
 def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -> int:
@@ -384,12 +389,10 @@ def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -
 
 def moe_expert_ffn_mxfp4(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales, act,
                          rows_max, d, F, E, seg_offsets, h_codes, h_scales, y_perm, ws, stream=None):
-    _on_gpu(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales, seg_offsets,
-            h_codes, h_scales, y_perm, ws)
+    operands = _on_gpu(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales)
+    seg, h, hs, y, wsp = _on_gpu(seg_offsets, h_codes, h_scales, y_perm, ws)
     _check("moe_expert_ffn_mxfp4", _lib.moe_expert_ffn_mxfp4(
-        _ptr(x_codes), _ptr(x_scales), _ptr(w1), _ptr(w1_scales), _ptr(w3), _ptr(w3_scales),
-        _ptr(w2), _ptr(w2_scales), act, int(rows_max), d, F, E, _ptr(seg_offsets), _ptr(h_codes),
-        _ptr(h_scales), _ptr(y_perm), _ptr(ws), ws.numel(), _stream(stream)))
+        *operands, act, int(rows_max), d, F, E, seg, h, hs, y, wsp, ws.numel(), _stream(stream)))
 
 
 def moe_ep_send_plan(kept_counts, seg_offsets, E, world, send_rows, send_offsets, ws, stream=None):

@@ -244,9 +244,13 @@ def test_binding_refuses_other_devices_and_strides(abi, monkeypatch):
         def stride(self):
             return (1, 2)
 
+        def data_ptr(self):
+            return 256 + self.device
+
     monkeypatch.setattr(abi, "_current_device", lambda: 0)
-    abi._on_gpu(Fake(0), None, Fake(0))
-    with pytest.raises(ValueError, match="current CUDA device"):
-        abi._on_gpu(Fake(0), Fake(1))
+    assert abi._on_gpu(Fake(0), None, Fake(0)) == [256, None, 256]
+    for others in ((Fake(0), Fake(1)), (Fake(1),), (Fake(0), Fake(-1)), (Fake(-1), Fake(0)), (None, Fake(-1))):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            abi._on_gpu(*others)
     with pytest.raises(ValueError, match="not contiguous"):
         abi._on_gpu(Fake(0), Fake(0, contiguous=False))
