@@ -153,7 +153,8 @@ typedef struct {
  * moe_mxfp4_quantize_weights writes them; the gather quantises the rows and
  * moe_expert_ffn_mxfp4 runs the experts. Router, x and out stay bf16. Not with
  * MOE_LAYER_GATHER_IN_GEMM or MOE_LAYER_COMBINE_IN_GEMM
- * (MOE_ERR_UNSUPPORTED). The views' x_perm and h are the codes. */
+ * (MOE_ERR_UNSUPPORTED). The views' x_perm and h are the codes
+ * (moe_mxfp4_dequantize_rows reads them back). */
 #define MOE_LAYER_MXFP4 32
 
 /* Device pointers into a moe_forward workspace where that call leaves its
@@ -177,6 +178,9 @@ typedef struct {
   void* y_perm;          /* [rows_max, d]; NULL with MOE_LAYER_COMBINE_IN_GEMM */
   int64_t rows_max;
   int64_t capacity;      /* C, or -1 when dropless */
+  /* written with MOE_LAYER_MXFP4 only: the scales of x_perm and h */
+  void* x_perm_scales;
+  void* h_scales;
 } moe_views_t;
 
 /* Human-readable name of a status code (static string). */

@@ -61,7 +61,8 @@ class MoeViewsC(ctypes.Structure):
     _fields_ = [(n, c_void_p) for n in ("topk_idx", "topk_w", "aux_loss", "z_loss", "counts", "bins",
                                         "kept_counts", "seg_offsets", "sorted_slot",
                                         "slot_to_row", "row_slot", "drop_mask", "x_perm", "h",
-                                        "y_perm")] + [("rows_max", c_int64), ("capacity", c_int64)]
+                                        "y_perm")] + [("rows_max", c_int64), ("capacity", c_int64),
+                                                     ("x_perm_scales", c_void_p), ("h_scales", c_void_p)]
 
 
 _SIGS = {

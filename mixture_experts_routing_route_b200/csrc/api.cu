@@ -802,6 +802,10 @@ moe_status_t moe_forward_views(const moe_layer_t* layer, int T, void* ws, size_t
   v->y_perm = f.y_perm;
   v->rows_max = f.rows_max;
   v->capacity = f.cap;
+  if (mxfp4(layer)) {
+    v->x_perm_scales = f.x_scales;
+    v->h_scales = f.h_scales;
+  }
   return MOE_OK;
 }
 

@@ -124,6 +124,10 @@ class MoeLayer:
             off = ptr - base
             return ws[off:off + n * es].view(dt).view(*shape)
 
+        def scales(ptr, K):
+            n = abi.moe_mxfp4_row_scales_size(R, self.E, K)
+            return view(ptr, n, torch.uint8, (n,)) if self.mxfp4 else None
+
         return {
             "topk_idx": view(v.topk_idx, S, torch.int32, (T, self.k)),
             "topk_w": view(v.topk_w, S, torch.float32, (T, self.k)),
@@ -143,6 +147,8 @@ class MoeLayer:
                        view(v.x_perm, R * self.d, self.dtype, (R, self.d)) if v.x_perm else None),
             "h": (view(v.h, R * self.F // 2, torch.uint8, (R, self.F // 2)) if self.mxfp4 else
                   view(v.h, R * self.F, self.dtype, (R, self.F))),
+            "x_perm_scales": scales(v.x_perm_scales, self.d),
+            "h_scales": scales(v.h_scales, self.F),
             # no y_perm when the down projection writes the output itself
             "y_perm": view(v.y_perm, R * self.d, self.dtype, (R, self.d)) if v.y_perm else None,
             "rows_max": R,

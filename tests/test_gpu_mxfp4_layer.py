@@ -100,6 +100,12 @@ def test_layer_is_its_stages(T):
     assert abi.moe_get_device_error(w) == 0
     assert torch.equal(v["x_perm"].reshape(-1), xc) and torch.equal(v["h"].reshape(-1), hc)
     assert torch.equal(v["y_perm"], y) and torch.equal(o, out)
+    # the views read back as values: what the stages' own buffers hold
+    for name, K, codes, scales in (("x_perm", d, xc, xs), ("h", F, hc, hs)):
+        got, ref = torch.empty(rows, K, device=DEV), torch.empty(rows, K, device=DEV)
+        abi.moe_mxfp4_dequantize_rows(v[name], v[name + "_scales"], v["seg_offsets"], E, rows, K, got, w)
+        abi.moe_mxfp4_dequantize_rows(codes, scales, v["seg_offsets"], E, rows, K, ref, w)
+        assert torch.equal(got, ref) and torch.isfinite(ref).all()
 
 
 def test_layer_in_a_graph_beside_the_bf16_layer():
