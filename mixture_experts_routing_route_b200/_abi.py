@@ -27,6 +27,7 @@ MOE_ACT_GELU, MOE_ACT_SWIGLU = 0, 1
 MOE_LAYER_GATHER_IN_GEMM, MOE_LAYER_BINNED, MOE_LAYER_Z_LOSS, MOE_LAYER_COMBINE_IN_GEMM = 1, 2, 4, 8
 MOE_LAYER_MXFP4 = 32
 DEVERR_EXPERT_RANGE, DEVERR_ROW_RANGE, DEVERR_TIMEOUT = 1, 2, 4
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
 class MoeError(RuntimeError):
@@ -159,10 +160,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: Optional[int] = None) -> int:
+    """device: the current one, where the caller knows it (see _device_of)."""
     if stream is None:
-        if _raw_stream is not None and _current_device is not None and torch.cuda.is_initialized():
-            return _raw_stream(_current_device())
+        if _raw_stream is not None and _current_device is not None and (device is not None
+                                                                        or torch.cuda.is_initialized()):
+            return _raw_stream(_current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -170,9 +173,9 @@ def _stream(stream) -> int:
 
 
 def _on_gpu(*tensors):
-    """The addresses of tensors (None: NULL). Refuses what would fault or be
-    misread on the GPU: a tensor that is not on the current device (its kernels
-    and streams are the current device's), or not contiguous."""
+    """The addresses of tensors (None: NULL). Refuses a tensor that is not on the
+    current device (its kernels and streams are the current device's), or not
+    contiguous; _addr checks type and size too."""
     current = None
     out = []
     for t in tensors:
@@ -189,6 +192,32 @@ def _on_gpu(*tensors):
             raise ValueError(f"tensor of shape {tuple(t.shape)} and strides {t.stride()} is not contiguous")
         out.append(t.data_ptr())
     return out
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """The current device, which t has to be on."""
+    d = t.get_device()
+    if d < 0 or d != (torch.cuda.current_device() if _current_device is None else _current_device()):
+        _on_gpu(t)
+    return d
+
+
+# One call per operand, all checks in one expression: a small call's time is
+# the host's (a loop over (tensor, dtype, n) took 0.4 us more of 7).
+def _addr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, device: int) -> Optional[int]:
+    """The address of t (None: NULL), which the library takes for n values of
+    dtype on this device, the current one. Refuses what it would misread or
+    what is too short for it. torch.uint8 stands for any type of one byte."""
+    if t is None:
+        return None
+    if t.get_device() == device and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    address, = _on_gpu(t)
+    if t.dtype is not dtype and not (dtype is torch.uint8 and t.dtype.itemsize == 1):
+        raise ValueError(f"tensor of {t.dtype} where {dtype} is read or written")
+    if t.numel() < n:
+        raise ValueError(f"tensor of shape {tuple(t.shape)} where {n} values are read or written")
+    return address
 
 
 def _check(fn: str, st: int):
@@ -336,17 +365,22 @@ def moe_combine(y_perm, topk_w, slot_to_row, T, d, k, rows_max, out, ws, stream=
 
 def moe_combine_backward(d_out, y_perm, topk_w, slot_to_row, T, d, k, rows_max, d_y_perm, d_topk_w,
                          ws, stream=None):
-    g, y, w, s2r, dy, dw, wsp = _on_gpu(d_out, y_perm, topk_w, slot_to_row, d_y_perm, d_topk_w, ws)
+    rows_max = int(rows_max)
+    dev, dt, slots, row_values = _device_of(d_out), d_out.dtype, T * k, rows_max * d
     _check("moe_combine_backward", _lib.moe_combine_backward(
-        g, y, w, s2r, dtype_code(d_out.dtype), T, d, k, int(rows_max), dy, dw, wsp, ws.numel(),
-        _stream(stream)))
+        _addr(d_out, dt, T * d, dev), _addr(y_perm, dt, row_values, dev), _addr(topk_w, _F32, slots, dev),
+        _addr(slot_to_row, _I32, slots, dev), dtype_code(dt), T, d, k, rows_max,
+        _addr(d_y_perm, dt, row_values, dev), _addr(d_topk_w, _F32, slots, dev), _addr(ws, _U8, 0, dev),
+        ws.numel(), _stream(stream, dev)))
 
 
 def moe_gather_backward(d_x_perm, slot_to_row, dx_in, T, d, k, rows_max, dx, ws, stream=None):
-    g, s2r, add, out, wsp = _on_gpu(d_x_perm, slot_to_row, dx_in, dx, ws)
+    rows_max = int(rows_max)
+    dev, dt = _device_of(dx), dx.dtype
     _check("moe_gather_backward", _lib.moe_gather_backward(
-        g, s2r, add, dtype_code(dx.dtype), T, d, k, int(rows_max), out, wsp, ws.numel(),
-        _stream(stream)))
+        _addr(d_x_perm, dt, rows_max * d, dev), _addr(slot_to_row, _I32, T * k, dev),
+        _addr(dx_in, dt, T * d, dev), dtype_code(dt), T, d, k, rows_max, _addr(dx, dt, T * d, dev),
+        _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))
 
 
 def moe_mxfp4_weight_scales_size(E: int, K: int, N: int) -> int:
@@ -358,30 +392,37 @@ def moe_mxfp4_row_scales_size(rows_max: int, E: int, K: int) -> int:
 
 
 def moe_mxfp4_quantize_weights(w, E, K, N, codes, scales, stream=None):
-    wp, c, sc = _on_gpu(w, codes, scales)
+    dev = _device_of(w)
     _check("moe_mxfp4_quantize_weights", _lib.moe_mxfp4_quantize_weights(
-        wp, dtype_code(w.dtype), E, K, N, c, sc, _stream(stream)))
+        _addr(w, w.dtype, E * K * N, dev), dtype_code(w.dtype), E, K, N, _addr(codes, _U8, E * N * K // 2, dev),
+        _addr(scales, _U8, moe_mxfp4_weight_scales_size(E, K, N), dev), _stream(stream, dev)))
 
 
 def moe_mxfp4_dequantize_weights(codes, scales, E, K, N, w, stream=None):
-    c, sc, wp = _on_gpu(codes, scales, w)
+    dev = _device_of(w)
     _check("moe_mxfp4_dequantize_weights", _lib.moe_mxfp4_dequantize_weights(
-        c, sc, dtype_code(w.dtype), E, K, N, wp, _stream(stream)))
+        _addr(codes, _U8, E * N * K // 2, dev), _addr(scales, _U8, moe_mxfp4_weight_scales_size(E, K, N), dev),
+        dtype_code(w.dtype), E, K, N, _addr(w, w.dtype, E * K * N, dev), _stream(stream, dev)))
 
 
 def moe_gather_mxfp4(x, T, d, k, slot_to_row, seg_offsets, E, rows_max, codes, scales, ws,
                      stream=None):
-    xp, s2r, seg, c, sc, wsp = _on_gpu(x, slot_to_row, seg_offsets, codes, scales, ws)
+    rows_max = int(rows_max)
+    dev, dt = _device_of(x), x.dtype
     _check("moe_gather_mxfp4", _lib.moe_gather_mxfp4(
-        xp, dtype_code(x.dtype), T, d, k, s2r, seg, E, int(rows_max), c, sc, wsp, ws.numel(),
-        _stream(stream)))
+        _addr(x, dt, T * d, dev), dtype_code(dt), T, d, k, _addr(slot_to_row, _I32, T * k, dev),
+        _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, _addr(codes, _U8, rows_max * d // 2, dev),
+        _addr(scales, _U8, (rows_max // 128 + E) * (d // 128) * 512, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _stream(stream, dev)))
 
 
 def moe_mxfp4_dequantize_rows(codes, scales, seg_offsets, E, rows_max, K, out, ws, stream=None):
-    c, sc, seg, o, wsp = _on_gpu(codes, scales, seg_offsets, out, ws)
+    rows_max = int(rows_max)
+    dev, dt = _device_of(out), out.dtype
     _check("moe_mxfp4_dequantize_rows", _lib.moe_mxfp4_dequantize_rows(
-        c, sc, seg, E, int(rows_max), K, dtype_code(out.dtype), o, wsp, ws.numel(),
-        _stream(stream)))
+        _addr(codes, _U8, rows_max * K // 2, dev), _addr(scales, _U8, (rows_max // 128 + E) * (K // 128) * 512, dev),
+        _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, K, dtype_code(dt),
+        _addr(out, dt, rows_max * K, dev), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))
 
 
 def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -> int:
@@ -390,10 +431,20 @@ def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -
 
 def moe_expert_ffn_mxfp4(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales, act,
                          rows_max, d, F, E, seg_offsets, h_codes, h_scales, y_perm, ws, stream=None):
-    operands = _on_gpu(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2_scales)
-    seg, h, hs, y, wsp = _on_gpu(seg_offsets, h_codes, h_scales, y_perm, ws)
+    rows_max = int(rows_max)
+    dev = _device_of(y_perm)
+    matrix, matrix_scales = E * d * F // 2, moe_mxfp4_weight_scales_size(E, d, F)  # the same for [E, F, d]
+    groups = rows_max // 128 + E
+    if act != MOE_ACT_SWIGLU:
+        w3 = w3_scales = None
     _check("moe_expert_ffn_mxfp4", _lib.moe_expert_ffn_mxfp4(
-        *operands, act, int(rows_max), d, F, E, seg, h, hs, y, wsp, ws.numel(), _stream(stream)))
+        _addr(x_codes, _U8, rows_max * d // 2, dev), _addr(x_scales, _U8, groups * (d // 128) * 512, dev),
+        _addr(w1, _U8, matrix, dev), _addr(w1_scales, _U8, matrix_scales, dev), _addr(w3, _U8, matrix, dev),
+        _addr(w3_scales, _U8, matrix_scales, dev), _addr(w2, _U8, matrix, dev),
+        _addr(w2_scales, _U8, matrix_scales, dev), act, rows_max, d, F, E, _addr(seg_offsets, _I32, E + 1, dev),
+        _addr(h_codes, _U8, rows_max * F // 2, dev), _addr(h_scales, _U8, groups * (F // 128) * 512, dev),
+        _addr(y_perm, torch.bfloat16, rows_max * d, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _stream(stream, dev)))
 
 
 def moe_ep_send_plan(kept_counts, seg_offsets, E, world, send_rows, send_offsets, ws, stream=None):
