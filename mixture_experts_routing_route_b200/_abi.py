@@ -220,9 +220,22 @@ def _addr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, device: int) ->
     return address
 
 
+def _host_addr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int) -> Optional[int]:
+    """_addr for a host buffer."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{t.dtype} tensor of shape {tuple(t.shape)} and strides {t.stride()} where {n} contiguous "
+                         f"values of {dtype} are read or written")
+    return t.data_ptr()
+
+
 def _check(fn: str, st: int):
     if st != MOE_OK:
         raise MoeError(fn, st, _lib.moe_status_string(st).decode())
+
+
+_DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
 
 
 def dtype_code(t: torch.dtype) -> int:
@@ -499,9 +512,10 @@ def moe_forward(layer: MoeLayerC, x, T, out, aux_loss, ws, stream=None, events=N
                 e.record(torch.cuda.current_stream() if stream is None else stream)
         arr = (c_void_p * 7)(*[e.cuda_event if e is not None else None for e in events])
         ev = ctypes.cast(arr, c_void_p)
+    dev, dt = _device_of(ws), _DTYPES[layer.dtype]
     _check("moe_forward", _lib.moe_forward(
-        ctypes.byref(layer), _ptr(x), T, _ptr(out), _ptr(aux_loss), _ptr(ws), ws.numel(),
-        _stream(stream), ev))
+        ctypes.byref(layer), _addr(x, dt, T * layer.d, dev), T, _addr(out, dt, T * layer.d, dev),
+        _addr(aux_loss, _F32, 1, dev), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev), ev))
 
 
 def moe_forward_views(layer: MoeLayerC, T: int, ws) -> MoeViewsC:
@@ -512,6 +526,7 @@ def moe_forward_views(layer: MoeLayerC, T: int, ws) -> MoeViewsC:
 
 
 def moe_forward_host(layer: MoeLayerC, x_host, T, out_host, aux_host, ws, stream=None):
+    dev, dt = _device_of(ws), _DTYPES[layer.dtype]
     _check("moe_forward_host", _lib.moe_forward_host(
-        ctypes.byref(layer), _ptr(x_host), T, _ptr(out_host), _ptr(aux_host), _ptr(ws),
-        ws.numel(), _stream(stream)))
+        ctypes.byref(layer), _host_addr(x_host, dt, T * layer.d), T, _host_addr(out_host, dt, T * layer.d),
+        _host_addr(aux_host, _F32, 1), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))

@@ -24,6 +24,16 @@ class MoeLayer:
         if not w1.is_cuda:
             raise ValueError("weights must be CUDA tensors")
         self.E, self.d, self.F = w1.shape
+        shapes = {"w_router": (w_router, (self.d, self.E)), "w2": (w2, (self.E, self.F, self.d))}
+        if w3 is not None and act == "swiglu":
+            shapes["w3"] = w3, (self.E, self.d, self.F)
+        for name, (w, shape) in shapes.items():
+            if tuple(w.shape) != shape:
+                raise ValueError(f"{name} of shape {tuple(w.shape)}, not {shape} as w1 has it")
+            if w.device != w1.device:
+                raise ValueError(f"{name} on {w.device}, w1 on {w1.device}")
+            if not mxfp4 and w.dtype != w1.dtype:
+                raise ValueError(f"{name} is {w.dtype}, w1 {w1.dtype}")
         self.k = k
         self.dtype = w1.dtype
         self.act = abi.MOE_ACT_SWIGLU if act == "swiglu" else abi.MOE_ACT_GELU
@@ -78,15 +88,27 @@ class MoeLayer:
             self._ws[key] = ws
         return self._ws[key]
 
+    def _tokens(self, x: torch.Tensor) -> int:
+        T = x.shape[0]
+        if x.numel() != T * self.d:
+            raise ValueError(f"x of shape {tuple(x.shape)}, not [T, {self.d}]")
+        return T
+
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
                 aux: Optional[torch.Tensor] = None, stream=None, events=None,
                 x_router: Optional[torch.Tensor] = None,
                 logit_noise: Optional[torch.Tensor] = None):
         """x_router: the router's own input (e.g. moe_router_jitter of x);
-        logit_noise: [T, E] fp32 added to the gate logits (training variants)."""
-        T = x.shape[0]
-        self.c.x_router = None if x_router is None else x_router.data_ptr()
-        self.c.logit_noise = None if logit_noise is None else logit_noise.data_ptr()
+        logit_noise: [T, E] fp32 added to the gate logits (training variants).
+        x, x_router and out have the layer's dtype, aux is fp32; tensors of
+        another type, shorter or strided raise ValueError."""
+        T = self._tokens(x)
+        if x_router is None and logit_noise is None:
+            self.c.x_router = self.c.logit_noise = None
+        else:
+            dev = abi._device_of(x)
+            self.c.x_router = abi._addr(x_router, self.dtype, T * self.d, dev)
+            self.c.logit_noise = abi._addr(logit_noise, torch.float32, T * self.E, dev)
         if out is None:
             out = torch.empty(T, self.d, dtype=self.dtype, device=x.device)
         if aux is None:
@@ -102,7 +124,7 @@ class MoeLayer:
         """Pinned host x in, pinned host out and aux back, all asynchronous on
         `stream`. Calls that overlap (double-buffered serving on two streams)
         pass different `slot`s so they use different workspaces."""
-        T = x_host.shape[0]
+        T = self._tokens(x_host)
         self.c.x_router = None
         self.c.logit_noise = None
         ws = self.workspace(T, host_io=True, stream=stream, slot=slot)
