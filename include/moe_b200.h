@@ -187,11 +187,13 @@ typedef struct {
 MOE_API const char* moe_status_string(moe_status_t status);
 
 /* Zero the control block (first 256 bytes) of a workspace, asynchronously
- * on `stream`. Needed once per workspace before its first use, and again
- * after a call reported MOE_DEVERR_TIMEOUT: a wait that gave up leaves the
- * grid-barrier words of the control block in an unknown state, and the next
- * call on that workspace could pass its barrier early. Zeroing also clears
- * the error word and restores the default wait limit. */
+ * on `stream` (one small kernel). Needed once per workspace before its first
+ * use, and again after a call reported MOE_DEVERR_TIMEOUT: a wait that gave up
+ * leaves the grid-barrier words of the control block in an unknown state, and
+ * the next call on that workspace could pass its barrier early. Zeroing also
+ * clears the error word and restores the default wait limit. Calls that may
+ * run at the same time (on two streams, or in two graphs) need a workspace
+ * each. */
 MOE_API moe_status_t moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Set how long a kernel using this workspace waits at a barrier between its

@@ -194,6 +194,22 @@ def _on_gpu(*tensors):
     return out
 
 
+_capture_info = None
+
+
+def _capture_id(handle: int) -> int:
+    """The capture into a graph that a stream is part of, 0 for none."""
+    global _capture_info
+    if _capture_info is None:
+        _capture_info = ctypes.CDLL("libcuda.so.1").cuStreamGetCaptureInfo_v2
+        _capture_info.argtypes = [c_void_p, ctypes.POINTER(c_int), ctypes.POINTER(ctypes.c_uint64)] + [c_void_p] * 3
+    status, which = c_int(0), ctypes.c_uint64(0)
+    # the error is that of the legacy stream while others capture: not part of it
+    if _capture_info(handle, status, which, None, None, None) != 0 or status.value == 0:
+        return 0
+    return which.value
+
+
 def _device_of(t: torch.Tensor) -> int:
     """The current device, which t has to be on."""
     d = t.get_device()

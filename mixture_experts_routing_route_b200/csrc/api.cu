@@ -298,7 +298,7 @@ uint64_t moe_kernel_launches(void) { return g_launches.load(std::memory_order_re
 moe_status_t moe_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
   MOE_NEED(ws);
   if (ws_bytes < sizeof(Control)) return MOE_ERR_WORKSPACE;
-  return from_cuda(cudaMemsetAsync(ws, 0, sizeof(Control), reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_init_control(static_cast<Control*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_workspace_set_wait_limit(void* ws, size_t ws_bytes, uint32_t limit_us,

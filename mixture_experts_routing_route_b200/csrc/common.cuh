@@ -317,7 +317,8 @@ cudaError_t launch_gather(const void* x, size_t elem, int T, int d, int k, const
                           cudaStream_t s, bool binned = false, const int32_t* slot_to_row = nullptr,
                           void* zero_out = nullptr);
 
-// Control block: write the wait limit (one thread).
+// Control block: zero it; write the wait limit (one small kernel each).
+cudaError_t launch_init_control(Control* ctl, cudaStream_t s);
 cudaError_t launch_set_wait_limit(Control* ctl, uint32_t limit_us, cudaStream_t s);
 
 // Grouped GEMMs. bf16: A is x_perm [rows_max, d] when row_slot is NULL, else

@@ -338,12 +338,25 @@ permute_grid_kernel(const int32_t* __restrict__ idx, int S, int E, unsigned key_
   if (has_job) finish_aux_job(job, ctl, s_e);  // the router's loss, spread over the CTAs
 }
 
+// A kernel and not a memset: a layer captured into a graph begins with it.
+// Between two kernels a memset node costs the graph 3 us, this one with its
+// early start under 1 us (a decode step of an MXFP4 layer of d 512, F 512: 29.8
+// us without, 32.5 and 30.2 us).
+__global__ void init_control_kernel(Control* ctl) {
+  pdl_begin();
+  reinterpret_cast<uint32_t*>(ctl)[threadIdx.x] = 0u;
+}
+
 __global__ void set_wait_limit_kernel(Control* ctl, uint32_t limit_us) {
   pdl_begin();
   ctl->wait_limit_us = limit_us;
 }
 
 }  // namespace
+
+cudaError_t launch_init_control(Control* ctl, cudaStream_t s) {
+  return launch_pdl(init_control_kernel, dim3(1), dim3(sizeof(Control) / 4), 0, s, false, ctl);
+}
 
 cudaError_t launch_set_wait_limit(Control* ctl, uint32_t limit_us, cudaStream_t s) {
   return launch_pdl(set_wait_limit_kernel, dim3(1), dim3(1), 0, s, false, ctl, limit_us);

@@ -74,19 +74,39 @@ class MoeLayer:
         self.c = abi.layer_struct(self.d, self.E, k, self.F, abi.dtype_code(self.dtype), self.act,
                                   self.cf, self.w_router, self.bias, self.w1, self.w3, self.w2,
                                   flags, router_temperature, self.scales)
+        # (T, host_io, slot, stream handle), whether captured into a graph: the capture's id, workspace
         self._ws = {}
+        self._last = {}  # (T, host_io, slot): the last call's
 
     def workspace(self, T: int, host_io: bool = False, stream=None, slot: int = 0) -> torch.Tensor:
-        """The device workspace for T tokens; `slot` keeps separate ones for
-        calls that may run at the same time on different streams."""
-        key = (T, host_io, slot)
-        if key not in self._ws:
+        """The device workspace of the last call with T tokens and this slot,
+        or (stream given) the one that calls on `stream` use. Calls on two
+        streams may run at the same time, so every stream has its own, and
+        calls that are captured into a graph have one in the graph's memory,
+        which every replay initialises; `slot` keeps more of them apart."""
+        if stream is None and (T, host_io, slot) in self._last:
+            return self._last[T, host_io, slot]
+        return self._workspace(T, host_io, stream, slot)
+
+    def _workspace(self, T: int, host_io: bool, stream, slot: int) -> torch.Tensor:
+        handle = abi._stream(stream)
+        key = T, host_io, slot, handle
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            capture = abi._capture_id(handle)
+        else:
+            capture = 0
+        made_in, ws = self._ws.get((key, capture != 0), (0, None))
+        if ws is None or made_in != capture:
             n = (abi.moe_forward_host_workspace_size(self.c, T) if host_io
                  else abi.moe_forward_workspace_size(self.c, T))
-            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.w1.device)
-            abi.moe_workspace_init(ws, stream)
-            self._ws[key] = ws
-        return self._ws[key]
+            if stream is not None and not isinstance(stream, torch.Stream):
+                stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            # allocated and initialised on the stream that uses it
+            with torch.cuda.stream(stream):
+                ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.w1.device)
+                abi.moe_workspace_init(ws)
+            self._ws[key, capture != 0] = capture, ws
+        return ws
 
     def _tokens(self, x: torch.Tensor) -> int:
         T = x.shape[0]
@@ -113,7 +133,7 @@ class MoeLayer:
             out = torch.empty(T, self.d, dtype=self.dtype, device=x.device)
         if aux is None:
             aux = torch.empty(1, dtype=torch.float32, device=x.device)
-        ws = self.workspace(T, stream=stream)
+        ws = self._last[T, False, 0] = self._workspace(T, False, stream, 0)
         abi.moe_forward(self.c, x, T, out, aux, ws, stream, events)
         return out, aux
 
@@ -122,20 +142,21 @@ class MoeLayer:
     def forward_host(self, x_host: torch.Tensor, out_host: torch.Tensor, aux_host: torch.Tensor,
                      stream=None, slot: int = 0):
         """Pinned host x in, pinned host out and aux back, all asynchronous on
-        `stream`. Calls that overlap (double-buffered serving on two streams)
-        pass different `slot`s so they use different workspaces."""
+        `stream`. Calls with different `slot`s use different workspaces on one
+        stream too (double-buffered serving)."""
         T = self._tokens(x_host)
         self.c.x_router = None
         self.c.logit_noise = None
-        ws = self.workspace(T, host_io=True, stream=stream, slot=slot)
+        ws = self._last[T, True, slot] = self._workspace(T, True, stream, slot)
         abi.moe_forward_host(self.c, x_host, T, out_host, aux_host, ws, stream)
 
     def device_error(self, T: int, stream=None) -> int:
         return abi.moe_get_device_error(self.workspace(T, stream=stream), stream)
 
-    def views(self, T: int) -> dict:
-        """Torch views of the intermediates moe_forward left in the workspace."""
-        ws = self.workspace(T)
+    def views(self, T: int, stream=None) -> dict:
+        """Torch views of the intermediates that the last forward of T tokens
+        (on `stream`, if given) left in its workspace."""
+        ws = self.workspace(T, stream=stream)
         v = abi.moe_forward_views(self.c, T, ws)
         base = ws.data_ptr()
         R = v.rows_max

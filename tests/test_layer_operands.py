@@ -30,7 +30,8 @@ def layer(abi, dtype):  # noqa: F811
     m = MoeLayer.__new__(MoeLayer)
     m.E, m.d, m.F, m.k, m.dtype = E, D, F, 2, dtype
     m.c = abi.MoeLayerC(D, E, 2, F, abi.dtype_code(dtype))
-    m.workspace = lambda *a, **k: Fake(U8, 1 << 20)
+    m.workspace = m._workspace = lambda *a, **k: Fake(U8, 1 << 20)
+    m._last = {}
     return m
 
 
