@@ -121,20 +121,21 @@ class MoeLayer:
         """x_router: the router's own input (e.g. moe_router_jitter of x);
         logit_noise: [T, E] fp32 added to the gate logits (training variants).
         x, x_router and out have the layer's dtype, aux is fp32; tensors of
-        another type, shorter or strided raise ValueError."""
+        another type, shorter or strided raise ValueError. Threads that call
+        one layer at the same time call it on different streams."""
         T = self._tokens(x)
-        if x_router is None and logit_noise is None:
-            self.c.x_router = self.c.logit_noise = None
-        else:
-            dev = abi._device_of(x)
-            self.c.x_router = abi._addr(x_router, self.dtype, T * self.d, dev)
-            self.c.logit_noise = abi._addr(logit_noise, torch.float32, T * self.E, dev)
+        c = self.c
+        if x_router is not None or logit_noise is not None:
+            # a struct of this call's: another thread's may read the layer's
+            c, dev = abi.MoeLayerC.from_buffer_copy(c), abi._device_of(x)
+            c.x_router = abi._addr(x_router, self.dtype, T * self.d, dev)
+            c.logit_noise = abi._addr(logit_noise, torch.float32, T * self.E, dev)
         if out is None:
             out = torch.empty(T, self.d, dtype=self.dtype, device=x.device)
         if aux is None:
             aux = torch.empty(1, dtype=torch.float32, device=x.device)
         ws = self._last[T, False, 0] = self._workspace(T, False, stream, 0)
-        abi.moe_forward(self.c, x, T, out, aux, ws, stream, events)
+        abi.moe_forward(c, x, T, out, aux, ws, stream, events)
         return out, aux
 
     __call__ = forward
@@ -145,8 +146,6 @@ class MoeLayer:
         `stream`. Calls with different `slot`s use different workspaces on one
         stream too (double-buffered serving)."""
         T = self._tokens(x_host)
-        self.c.x_router = None
-        self.c.logit_noise = None
         ws = self._last[T, True, slot] = self._workspace(T, True, stream, slot)
         abi.moe_forward_host(self.c, x_host, T, out_host, aux_host, ws, stream)
 

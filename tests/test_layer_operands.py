@@ -51,10 +51,11 @@ def forward_host(m, dtype, **over):
 def test_forward(abi, reached, dtype):  # noqa: F811
     m = layer(abi, dtype)
     forward(m, dtype, x_router=Tokens(dtype, T, address=512), logit_noise=Tokens(F32, T, E, address=768))
-    assert (m.c.x_router, m.c.logit_noise) == (512, 768)
     forward(m, dtype)
     assert len(reached) == 2 and reached[1][1] == 4096 and reached[1][3] == 8192
-    assert m.c.x_router is None and m.c.logit_noise is None
+    structs = [args[0]._obj for args in reached]
+    assert (structs[0].x_router, structs[0].logit_noise) == (512, 768) and structs[0].d == D
+    assert structs[1].x_router is None and structs[1].logit_noise is None
     other = F32 if dtype is BF16 else BF16
     for wrong in (dict(x=Tokens(other, T)), dict(x=Tokens(dtype, T, D - 128)), dict(x=Tokens(dtype, 2, 3 * D)),
                   dict(x=Tokens(dtype, T, device=-1)), dict(x=Tokens(dtype, T, contiguous=False)),
@@ -65,6 +66,23 @@ def test_forward(abi, reached, dtype):  # noqa: F811
         with pytest.raises(ValueError):
             forward(m, dtype, **wrong)
     assert len(reached) == 2
+
+
+def test_two_calls_at_once(abi, reached, monkeypatch):  # noqa: F811
+    """A forward that begins while another one is in the library leaves it its router input."""
+    m = layer(abi, BF16)
+    seen = []
+
+    def library(c, *rest):
+        if not seen:
+            seen.append("in")
+            forward(m, BF16)
+        seen.append((c._obj.x_router, c._obj.logit_noise))
+        return 0
+
+    monkeypatch.setattr(abi._lib, "moe_forward", library)
+    forward(m, BF16, x_router=Tokens(BF16, T, address=512), logit_noise=Tokens(F32, T, E, address=768))
+    assert seen == ["in", (None, None), (512, 768)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
