@@ -39,6 +39,7 @@ class MoeLayer:
         self.act = abi.MOE_ACT_SWIGLU if act == "swiglu" else abi.MOE_ACT_GELU
         self.cf = float(capacity_factor)
         self.w_router = w_router.contiguous()
+        self.bias = None if bias is None else bias.to(device=w1.device, dtype=torch.float32).contiguous()
         # mxfp4: the experts in microscaled 4-bit floating point
         # (MOE_LAYER_MXFP4); the weights given (bf16 or fp32) are quantised here
         # and only their codes and scales are kept. x and out are bf16.
@@ -51,14 +52,14 @@ class MoeLayer:
             self.w3, s3 = (None, None) if w3 is None else abi.quantize_expert_weights(w3)
             self.w2, s2 = abi.quantize_expert_weights(w2)
             self.scales = (s1, s3, s2)
-            # forward may be called on any stream
+            # forward may be called on any stream: all of the layer's tensors
+            # are complete from here on
             torch.cuda.current_stream().synchronize()
         else:
             self.w1 = w1.contiguous()
             self.w3 = None if w3 is None else w3.contiguous()
             self.w2 = w2.contiguous()
             self.scales = (None, None, None)
-        self.bias = None if bias is None else bias.to(device=w1.device, dtype=torch.float32).contiguous()
         # gather_in_gemm: the up projection gathers x rows itself (bf16; see
         # MOE_LAYER_GATHER_IN_GEMM in include/moe_b200.h)
         # binned: the [E, C, hs] bucket layout (MOE_LAYER_BINNED); with
