@@ -142,7 +142,8 @@ FwdLayout fwd_layout(const moe_layer_t* L, int T, void* ws, bool host_io) {
     f.x_scales = static_cast<uint8_t*>(c.take(moe_mxfp4_row_scales_size(f.rows_max, L->E, L->d)));
     f.h = c.take(R * L->F / 2);
     f.h_scales = static_cast<uint8_t*>(c.take(moe_mxfp4_row_scales_size(f.rows_max, L->E, L->F)));
-    f.mx_partials = f.rows_max <= kMxStreamRows ? static_cast<float*>(c.take(mxfp4_stream_partials_bytes())) : nullptr;
+    const bool few = mxfp4_rows(f.rows_max, static_cast<int64_t>(S)) <= kMxStreamRows;
+    f.mx_partials = few ? static_cast<float*>(c.take(mxfp4_stream_partials_bytes())) : nullptr;
   } else {
     f.x_perm = gather_in_gemm(L) ? nullptr : c.take(R * L->d * es);
     f.h = c.take(R * L->F * es);
@@ -244,7 +245,7 @@ moe_status_t run_forward(const moe_layer_t* L, const void* x, int T, void* out, 
     MOE_CHECK(from_cuda(launch_ffn_mxfp4(xq, weights(L->w1, L->w1_scales), weights(L->w3, L->w3_scales),
                                          weights(L->w2, L->w2_scales), L->act, f.rows_max, L->d, L->F, L->E, f.seg,
                                          binned(L) ? f.kept : nullptr, hq, f.y_perm, f.mx_partials, f.ctl, s, after_up,
-                                         /*early_up=*/true)));
+                                         /*early_up=*/true, static_cast<int64_t>(T) * L->k)));
   } else if (L->dtype == MOE_BF16) {
     const bool g = gather_in_gemm(L);
     const CombineOut co{f.row_slot, f.w, out, T};

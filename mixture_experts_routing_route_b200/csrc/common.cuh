@@ -390,13 +390,20 @@ cudaError_t launch_mxfp4_dequantize_rows(const uint8_t* codes, const uint8_t* sc
                                          int E, int64_t rows_max, int K, moe_dtype_t dt, void* out,
                                          Control* ctl, cudaStream_t s);
 // The experts' FFN on MXFP4 rows and weights; y bf16. kept: rows of each
-// expert (binned layout), NULL: seg[e + 1] - seg[e]. partials:
-// mxfp4_stream_partials_bytes() when rows_max <= kMxStreamRows. early_up: seg,
-// kept and the weights were complete before the last kernel on s began.
+// expert (binned layout), NULL: seg[e + 1] - seg[e]. early_up: seg, kept and the
+// weights were complete before the last kernel on s began. slots: rows that the
+// permute distributes over the experts (T * k), negative: rows_max. At most
+// mxfp4_rows(rows_max, slots) rows are in use, in the dense and in the binned
+// layout (whose rows_max counts the padding too); this number picks the kernels,
+// so both layouts run the same ones. partials: mxfp4_stream_partials_bytes()
+// when it is at most kMxStreamRows.
+inline int64_t mxfp4_rows(int64_t rows_max, int64_t slots) {
+  return slots >= 0 && slots < rows_max ? slots : rows_max;
+}
 cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
                              moe_act_t act, int64_t rows_max, int d, int F, int E, const int32_t* seg,
                              const int32_t* kept, const MxRows& h, void* y, float* partials, Control* ctl,
-                             cudaStream_t s, cudaEvent_t after_up, bool early_up = false);
+                             cudaStream_t s, cudaEvent_t after_up, bool early_up = false, int64_t slots = -1);
 
 // Expert-parallel dispatch plans (ep.cu). Experts are owned in contiguous
 // blocks of e_loc per rank.

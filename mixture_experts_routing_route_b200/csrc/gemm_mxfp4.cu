@@ -602,22 +602,24 @@ cudaError_t run_group(const MxRows& a, const MxWeights& b0, const MxWeights& b1,
     return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::SMEM, s, false, ta, tb0, tb1, sa, sb0, sb1, args);
 }
 
-// A product runs on CTA pairs where experts have many rows on average (of
-// rows_max, which is all the host knows) and K is long; single CTAs' 128-row
-// tiles fill better, and with short K a tile's turnaround counts, which the
-// second CTA lengthens. Measured, whole FFN, single against pairs for both
-// products: 8 experts, d 4096, F 14336: 32 rows an expert 131 / 154 us, 128 rows
-// 166 / 159, 256 rows 229 / 220, 512 rows 377 / 350, 1024 rows 659 / 570; 64
-// experts, d 4096, F 2048, skewed, 128 rows 182 / 208, 512 rows 469 / 457; d
-// 2048, F 1408: 256 rows 116 / 115, 512 rows 189 / 181. With d 1024, F 4096, 512
-// rows: singles 195, pairs for the down projection alone 191, for both 195; if a
-// capacity leaves 173 of the 512: 91, 92, 102.
+// A product runs on CTA pairs where experts have many rows on average (of the
+// most that can be in use, which is all the host knows) and K is long; single
+// CTAs' 128-row tiles fill better, and with short K a tile's turnaround counts,
+// which the second CTA lengthens. Measured, whole FFN, single against pairs for
+// both products, short runs at 1.7 GHz and up (in a loop under the power cap, at
+// 1.4 to 1.5 GHz, both take a sixth longer): 8 experts, d 4096, F 14336: 32 rows
+// an expert 131 / 154 us, 128 rows 166 / 159, 256 rows 229 / 220, 512 rows 377 /
+// 350, 1024 rows 659 / 570; 64 experts, d 4096, F 2048, skewed, 128 rows 182 /
+// 208, 512 rows 469 / 457; d 2048, F 1408: 256 rows 116 / 115, 512 rows 189 /
+// 181. With d 1024, F 4096, 512 rows: singles 195, pairs for the down projection
+// alone 191, for both 195; if a capacity leaves 173 of the 512: 91, 92, 102.
 constexpr int64_t kPairRows = 256;
 constexpr int kPairK = 2048;
 
 template <int EPI, int NMMA>
-cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, cudaStream_t s) {
-  if (args.rows_max >= kPairRows * args.E && args.K >= kPairK) return run_group<EPI, NMMA, 2>(a, b0, b1, args, s);
+cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, const MxArgs& args, int64_t rows,
+                     cudaStream_t s) {
+  if (rows >= kPairRows * args.E && args.K >= kPairK) return run_group<EPI, NMMA, 2>(a, b0, b1, args, s);
   return run_group<EPI, NMMA, 1>(a, b0, b1, args, s);
 }
 
@@ -626,7 +628,7 @@ cudaError_t run_gemm(const MxRows& a, const MxWeights& b0, const MxWeights& b1, 
 cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeights& w3, const MxWeights& w2,
                              moe_act_t act, int64_t rows_max, int d, int F, int E, const int32_t* seg,
                              const int32_t* kept, const MxRows& h, void* y, float* partials, Control* ctl,
-                             cudaStream_t s, cudaEvent_t after_up, bool early_up) {
+                             cudaStream_t s, cudaEvent_t after_up, bool early_up, int64_t slots) {
   if (rows_max <= 0) {
     if (after_up) cudaEventRecord(after_up, s);
     return cudaSuccess;
@@ -643,10 +645,11 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.out_codes = h.codes;
   a.out_scales = h.scales;
   a.out = static_cast<__nv_bfloat16*>(y);
+  const int64_t rows = mxfp4_rows(rows_max, slots);
   // A decode step's rows (32 at most, so no expert has more) go through the
   // weight stream: one token of a Mixtral-shaped layer takes 44 us there,
   // 57 us here.
-  if (rows_max <= kMxStreamRows) {
+  if (rows <= kMxStreamRows) {
     a.partials = partials;
     const cudaError_t err = launch_stream_ffn_mxfp4(x, w1, w3, w2, act, h, a, s);
     if (after_up) cudaEventRecord(after_up, s);
@@ -656,18 +659,18 @@ cudaError_t launch_ffn_mxfp4(const MxRows& x, const MxWeights& w1, const MxWeigh
   a.N = F;
   cudaError_t err;
   if (act == MOE_ACT_SWIGLU)
-    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, s);
+    err = run_gemm<EPI_SWIGLU, 256>(x, w1, w3, a, rows, s);
   else if (F % 256 == 0)
-    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, s);
+    err = run_gemm<EPI_GELU, 256>(x, w1, w1, a, rows, s);
   else
-    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, s);
+    err = run_gemm<EPI_GELU, 128>(x, w1, w1, a, rows, s);
   if (err != cudaSuccess) return err;
   if (after_up) cudaEventRecord(after_up, s);
   a.early = 1;
   a.K = F;
   a.N = d;
-  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, s);
-  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, s);
+  if (d % 256 == 0) return run_gemm<EPI_STORE, 256>(h, w2, w2, a, rows, s);
+  return run_gemm<EPI_STORE, 128>(h, w2, w2, a, rows, s);
 }
 
 }  // namespace moe
