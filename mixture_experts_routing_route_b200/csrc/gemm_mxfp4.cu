@@ -188,12 +188,21 @@ __device__ __forceinline__ void epilogue(uint32_t tbase, const MxArgs& args, con
       tmem_ld_32x32b_x32(tbase + 32 * g, v);
       tmem_ld_wait();
       if (gi == 0) free_overlap();
+      auto activate = [&](auto phi) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float a = __uint_as_float(v[i]), b = __uint_as_float(v[i + 1]);
-        const float2 r = EPI == EPI_GELU ? gelu_fast2(a, b) : make_float2(a, b);
-        h[i] = r.x;
-        h[i + 1] = r.y;
+        for (int i = 0; i < 32; i += 2) {
+          const float2 r = gelu2<decltype(phi)>(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          h[i] = r.x;
+          h[i + 1] = r.y;
+        }
+      };
+      if constexpr (EPI == EPI_GELU) {
+        if (gelu_tail(v)) activate(PhiTail{});
+        else activate(Phi{});
+        __syncwarp();  // the next loads from tensor memory are the whole warp's
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) h[i] = __uint_as_float(v[i]);
       }
     }
     const int col = t.n0 + 32 * g;

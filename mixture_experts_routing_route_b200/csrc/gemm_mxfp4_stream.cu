@@ -505,7 +505,7 @@ stream_ffn_mxf4(const __grid_constant__ StreamMaps maps, MxArgs args) {
               if constexpr (EPI == EPI_STORE) {
                 args.out[row * args.d + t.n0 + col] = __float2bfloat16_rn(v[0][k]);
               } else {
-                const float h = EPI == EPI_SWIGLU ? silu_fast(v[0][k]) * v[MATS - 1][k] : gelu_fast2(v[0][k], 0.0f).x;
+                const float h = EPI == EPI_SWIGLU ? silu_fast(v[0][k]) * v[MATS - 1][k] : gelu2<PhiTail>(v[0][k], 0.0f).x;
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
                 const uint32_t sb = mx_scale_byte(top);
                 // eight lanes' codes to one word

@@ -45,13 +45,14 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// The up projection's activations. Their result is rounded to E2M1, so a few
-// ulp never show; a tile has up to 32768 of them, and they bound the kernel
-// where K is short (with erff the epilogue of a 128 x 256 tile took 11500
-// cycles, the MMAs of K = 1024 2400).
+// The up projection's activations. Their result is rounded to E2M1 with a scale
+// of its block's own, so what counts is the error relative to the largest value
+// of the block. A tile has up to 32768 of them, and they bound the kernel where K
+// is short (with erff the epilogue of a 128 x 256 tile took 11500 cycles, the
+// MMAs of K = 1024 2400).
 //
-// silu(g) = g / (1 + e^-g): for g < -128 ln 2 the exponential is Inf, its
-// reciprocal 0 and the result -0, the limit.
+// silu(g) = g / (1 + e^-g): for g < -126 ln 2 the reciprocal is subnormal or 0
+// and the result -0 (its value is below 2^-119).
 __device__ __forceinline__ float silu_fast(float g) { return g * rcp(1.0f + ex2(-1.44269504f * g)); }
 
 // Two fp32 values in one 64-bit register pair, for the packed instructions (two
@@ -78,23 +79,62 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 
 // gelu(z) = z Phi(z) = max(z, 0) - |z| Phi(-|z|). log2 Phi(-a) is nearly a
-// parabola, so a polynomial of degree 5 is enough: the one with the smallest
-// largest error of Phi on [0, 6.5], 2.9e-7, found by linear programming. It
-// falls on from there, to 2^-35 and below. In fp32 the result is within 3.5e-7
-// |z|. One special function (8 cycles) and six multiply-adds a value: with a
-// reciprocal and eleven (Abramowitz and Stegun 7.1.28, 1.1e-6 |z|) an epilogue of
-// 128 x 256 values took 5000 cycles, with both special functions (7.1.26) 6300.
-// Two values at a time.
-__device__ __forceinline__ float2 gelu_fast2(float z0, float z1) {
+// parabola, and 2^p(a) with a polynomial p gives Phi(-a); its coefficients were
+// found by linear programming, and both leave 0 beyond a = 13. Two values at a
+// time.
+//
+// Phi, degree 5: the smallest largest error of Phi on [0, 6.5], 2.9e-7; in fp32
+// gelu is within 3.7e-7 |z|. One special function (8 cycles) and six
+// multiply-adds a value: with a reciprocal and eleven (Abramowitz and Stegun
+// 7.1.28, 1.1e-6 |z|) an epilogue of 128 x 256 values took 5000 cycles, with both
+// special functions (7.1.26) 6300. Relative to Phi(-a) it is within 8e-6 for a up
+// to 2, 3e-5 to 2.5, 6e-5 to 3, but 6e-3 to 4 and 5e-2 to 5.
+//
+// PhiTail, degree 12: relative to Phi(-a), in fp32, within 1.7e-6 for a up to 3,
+// 5.5e-6 to 6, 1.2e-5 to 8, 3.5e-5 to 10, 2.2e-4 to 13. For blocks of h that lie
+// in the tail altogether. In all others (a value of at least 0.3, whose gelu is
+// 0.18, or none below -2.5) what is below -2.9 has the code 0, since |gelu| is
+// less than a 32nd of the block's largest: Phi is within 6e-5 of the rest.
+struct Phi {
+  static constexpr int N = 6;
+  static __device__ __forceinline__ constexpr float c(int i) {
+    constexpr float v[N] = {-1.0000008f, -1.1510831f, -0.45927668f, -0.052538015f, 0.0073872f, -0.0005188585f};
+    return v[i];
+  }
+};
+struct PhiTail {
+  static constexpr int N = 13;
+  static __device__ __forceinline__ constexpr float c(int i) {
+    constexpr float v[N] = {-0.999998033f,    -1.15117109f,     -0.458849788f,   -0.0532412268f,  0.0078255767f,
+                            -0.000555978215f, -6.54001778e-05f, 2.56033727e-05f, -3.80394295e-06f, 3.34066243e-07f,
+                            -1.79620532e-08f, 5.47664081e-10f,  -7.26788898e-12f};
+    return v[i];
+  }
+};
+
+template <typename P>
+__device__ __forceinline__ float2 gelu2(float z0, float z1) {
   const float a0 = fabsf(z0), a1 = fabsf(z1);
   const uint64_t a = pack2(a0, a1);
-  uint64_t p = fma2(a, pack2(-0.0005188585f, -0.0005188585f), pack2(0.0073872f, 0.0073872f));
-  p = fma2(p, a, pack2(-0.052538015f, -0.052538015f));
-  p = fma2(p, a, pack2(-0.45927668f, -0.45927668f));
-  p = fma2(p, a, pack2(-1.1510831f, -1.1510831f));
-  p = fma2(p, a, pack2(-1.0000008f, -1.0000008f));
+  uint64_t p = pack2(P::c(P::N - 1), P::c(P::N - 1));
+#pragma unroll
+  for (int i = P::N - 2; i >= 0; --i) p = fma2(p, a, pack2(P::c(i), P::c(i)));
   const float2 q = unpack2(p);
   return make_float2(fmaf(-a0, ex2(q.x), fmaxf(z0, 0.0f)), fmaf(-a1, ex2(q.y), fmaxf(z1, 0.0f)));
+}
+
+// Whether a block of h (32 values z of one row) needs PhiTail. Its second half
+// is rarely reached.
+__device__ __forceinline__ bool gelu_tail(const uint32_t (&z)[32]) {
+  float low = __uint_as_float(z[0]);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2)
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(low) : "f"(__uint_as_float(z[i])), "f"(__uint_as_float(z[i + 1])));
+  if (fminf(low, __uint_as_float(z[31])) >= -2.5f) return false;
+  float high = __uint_as_float(z[0]);
+#pragma unroll
+  for (int i = 1; i < 32; ++i) high = fmaxf(high, __uint_as_float(z[i]));
+  return high < 0.3f;
 }
 
 // ------------------------------------------------------------ tcgen05, mxf4
