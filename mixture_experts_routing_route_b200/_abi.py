@@ -156,16 +156,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 # The current stream's handle without building a torch.cuda.Stream (3 us of a
 # 9 us call); the public way where this torch has no such function.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream, device: Optional[int] = None) -> int:
-    """device: the current one, where the caller knows it (see _device_of)."""
+def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None and _current_device is not None and (device is not None
-                                                                        or torch.cuda.is_initialized()):
-            return _raw_stream(_current_device() if device is None else device)
+        if torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -185,7 +184,7 @@ def _on_gpu(*tensors):
         d = t.get_device()
         if d != current:
             if current is None and d >= 0:
-                current = torch.cuda.current_device() if _current_device is None else _current_device()
+                current = _current_device()
             if d != current:
                 raise ValueError(f"tensor on {t.device}, not on the current CUDA device")
         if not t.is_contiguous():
@@ -213,13 +212,14 @@ def _capture_id(handle: int) -> int:
 def _device_of(t: torch.Tensor) -> int:
     """The current device, which t has to be on."""
     d = t.get_device()
-    if d < 0 or d != (torch.cuda.current_device() if _current_device is None else _current_device()):
+    if d < 0 or d != _current_device():
         _on_gpu(t)
     return d
 
 
-# One call per operand, all checks in one expression: a small call's time is
-# the host's (a loop over (tensor, dtype, n) took 0.4 us more of 7).
+# One call per operand, all checks in one expression, and the wrappers look up
+# the dtype's code and the current stream without a call of their own: a small
+# call's time is the host's (a loop over (tensor, dtype, n) took 0.4 us of 7).
 def _addr(t: Optional[torch.Tensor], dtype: torch.dtype, n: int, device: int) -> Optional[int]:
     """The address of t (None: NULL), which the library takes for n values of
     dtype on this device, the current one. Refuses what it would misread or
@@ -251,15 +251,17 @@ def _check(fn: str, st: int):
         raise MoeError(fn, st, _lib.moe_status_string(st).decode())
 
 
-_DTYPES = {MOE_BF16: torch.bfloat16, MOE_F32: torch.float32}
+class _Codes(dict):
+    def __missing__(self, t):
+        raise ValueError(f"unsupported dtype {t}")
+
+
+_CODES = _Codes({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
+_DTYPES = {code: t for t, code in _CODES.items()}
 
 
 def dtype_code(t: torch.dtype) -> int:
-    if t == torch.bfloat16:
-        return MOE_BF16
-    if t == torch.float32:
-        return MOE_F32
-    raise ValueError(f"unsupported dtype {t}")
+    return _CODES[t]
 
 
 def status_string(st: int) -> str:
@@ -396,20 +398,24 @@ def moe_combine_backward(d_out, y_perm, topk_w, slot_to_row, T, d, k, rows_max, 
                          ws, stream=None):
     rows_max = int(rows_max)
     dev, dt, slots, row_values = _device_of(d_out), d_out.dtype, T * k, rows_max * d
-    _check("moe_combine_backward", _lib.moe_combine_backward(
+    st = _lib.moe_combine_backward(
         _addr(d_out, dt, T * d, dev), _addr(y_perm, dt, row_values, dev), _addr(topk_w, _F32, slots, dev),
-        _addr(slot_to_row, _I32, slots, dev), dtype_code(dt), T, d, k, rows_max,
+        _addr(slot_to_row, _I32, slots, dev), _CODES[dt], T, d, k, rows_max,
         _addr(d_y_perm, dt, row_values, dev), _addr(d_topk_w, _F32, slots, dev), _addr(ws, _U8, 0, dev),
-        ws.numel(), _stream(stream, dev)))
+        ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_combine_backward", st)
 
 
 def moe_gather_backward(d_x_perm, slot_to_row, dx_in, T, d, k, rows_max, dx, ws, stream=None):
     rows_max = int(rows_max)
     dev, dt = _device_of(dx), dx.dtype
-    _check("moe_gather_backward", _lib.moe_gather_backward(
+    st = _lib.moe_gather_backward(
         _addr(d_x_perm, dt, rows_max * d, dev), _addr(slot_to_row, _I32, T * k, dev),
-        _addr(dx_in, dt, T * d, dev), dtype_code(dt), T, d, k, rows_max, _addr(dx, dt, T * d, dev),
-        _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))
+        _addr(dx_in, dt, T * d, dev), _CODES[dt], T, d, k, rows_max, _addr(dx, dt, T * d, dev),
+        _addr(ws, _U8, 0, dev), ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_gather_backward", st)
 
 
 def moe_mxfp4_weight_scales_size(E: int, K: int, N: int) -> int:
@@ -422,36 +428,47 @@ def moe_mxfp4_row_scales_size(rows_max: int, E: int, K: int) -> int:
 
 def moe_mxfp4_quantize_weights(w, E, K, N, codes, scales, stream=None):
     dev = _device_of(w)
-    _check("moe_mxfp4_quantize_weights", _lib.moe_mxfp4_quantize_weights(
-        _addr(w, w.dtype, E * K * N, dev), dtype_code(w.dtype), E, K, N, _addr(codes, _U8, E * N * K // 2, dev),
-        _addr(scales, _U8, moe_mxfp4_weight_scales_size(E, K, N), dev), _stream(stream, dev)))
+    st = _lib.moe_mxfp4_quantize_weights(
+        _addr(w, w.dtype, E * K * N, dev), _CODES[w.dtype], E, K, N, _addr(codes, _U8, E * N * K // 2, dev),
+        _addr(scales, _U8, moe_mxfp4_weight_scales_size(E, K, N), dev),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_mxfp4_quantize_weights", st)
 
 
 def moe_mxfp4_dequantize_weights(codes, scales, E, K, N, w, stream=None):
     dev = _device_of(w)
-    _check("moe_mxfp4_dequantize_weights", _lib.moe_mxfp4_dequantize_weights(
+    st = _lib.moe_mxfp4_dequantize_weights(
         _addr(codes, _U8, E * N * K // 2, dev), _addr(scales, _U8, moe_mxfp4_weight_scales_size(E, K, N), dev),
-        dtype_code(w.dtype), E, K, N, _addr(w, w.dtype, E * K * N, dev), _stream(stream, dev)))
+        _CODES[w.dtype], E, K, N, _addr(w, w.dtype, E * K * N, dev),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_mxfp4_dequantize_weights", st)
 
 
 def moe_gather_mxfp4(x, T, d, k, slot_to_row, seg_offsets, E, rows_max, codes, scales, ws,
                      stream=None):
     rows_max = int(rows_max)
     dev, dt = _device_of(x), x.dtype
-    _check("moe_gather_mxfp4", _lib.moe_gather_mxfp4(
-        _addr(x, dt, T * d, dev), dtype_code(dt), T, d, k, _addr(slot_to_row, _I32, T * k, dev),
+    st = _lib.moe_gather_mxfp4(
+        _addr(x, dt, T * d, dev), _CODES[dt], T, d, k, _addr(slot_to_row, _I32, T * k, dev),
         _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, _addr(codes, _U8, rows_max * d // 2, dev),
         _addr(scales, _U8, (rows_max // 128 + E) * (d // 128) * 512, dev), _addr(ws, _U8, 0, dev), ws.numel(),
-        _stream(stream, dev)))
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_gather_mxfp4", st)
 
 
 def moe_mxfp4_dequantize_rows(codes, scales, seg_offsets, E, rows_max, K, out, ws, stream=None):
     rows_max = int(rows_max)
     dev, dt = _device_of(out), out.dtype
-    _check("moe_mxfp4_dequantize_rows", _lib.moe_mxfp4_dequantize_rows(
+    st = _lib.moe_mxfp4_dequantize_rows(
         _addr(codes, _U8, rows_max * K // 2, dev), _addr(scales, _U8, (rows_max // 128 + E) * (K // 128) * 512, dev),
-        _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, K, dtype_code(dt),
-        _addr(out, dt, rows_max * K, dev), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))
+        _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, K, _CODES[dt],
+        _addr(out, dt, rows_max * K, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_mxfp4_dequantize_rows", st)
 
 
 def moe_expert_ffn_mxfp4_workspace_size(rows_max: int, d: int, F: int, E: int) -> int:
@@ -466,14 +483,16 @@ def moe_expert_ffn_mxfp4(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2
     groups = rows_max // 128 + E
     if act != MOE_ACT_SWIGLU:
         w3 = w3_scales = None
-    _check("moe_expert_ffn_mxfp4", _lib.moe_expert_ffn_mxfp4(
+    st = _lib.moe_expert_ffn_mxfp4(
         _addr(x_codes, _U8, rows_max * d // 2, dev), _addr(x_scales, _U8, groups * (d // 128) * 512, dev),
         _addr(w1, _U8, matrix, dev), _addr(w1_scales, _U8, matrix_scales, dev), _addr(w3, _U8, matrix, dev),
         _addr(w3_scales, _U8, matrix_scales, dev), _addr(w2, _U8, matrix, dev),
         _addr(w2_scales, _U8, matrix_scales, dev), act, rows_max, d, F, E, _addr(seg_offsets, _I32, E + 1, dev),
         _addr(h_codes, _U8, rows_max * F // 2, dev), _addr(h_scales, _U8, groups * (F // 128) * 512, dev),
         _addr(y_perm, torch.bfloat16, rows_max * d, dev), _addr(ws, _U8, 0, dev), ws.numel(),
-        _stream(stream, dev)))
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_expert_ffn_mxfp4", st)
 
 
 def moe_ep_send_plan(kept_counts, seg_offsets, E, world, send_rows, send_offsets, ws, stream=None):
@@ -528,10 +547,14 @@ def moe_forward(layer: MoeLayerC, x, T, out, aux_loss, ws, stream=None, events=N
                 e.record(torch.cuda.current_stream() if stream is None else stream)
         arr = (c_void_p * 7)(*[e.cuda_event if e is not None else None for e in events])
         ev = ctypes.cast(arr, c_void_p)
-    dev, dt = _device_of(ws), _DTYPES[layer.dtype]
-    _check("moe_forward", _lib.moe_forward(
+    # (a dtype that is neither is the library's to refuse)
+    dev, dt = _device_of(ws), _DTYPES.get(layer.dtype, x.dtype)
+    st = _lib.moe_forward(
         ctypes.byref(layer), _addr(x, dt, T * layer.d, dev), T, _addr(out, dt, T * layer.d, dev),
-        _addr(aux_loss, _F32, 1, dev), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev), ev))
+        _addr(aux_loss, _F32, 1, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _raw_stream(dev) if stream is None else _stream(stream), ev)
+    if st != MOE_OK:
+        _check("moe_forward", st)
 
 
 def moe_forward_views(layer: MoeLayerC, T: int, ws) -> MoeViewsC:
@@ -542,7 +565,10 @@ def moe_forward_views(layer: MoeLayerC, T: int, ws) -> MoeViewsC:
 
 
 def moe_forward_host(layer: MoeLayerC, x_host, T, out_host, aux_host, ws, stream=None):
-    dev, dt = _device_of(ws), _DTYPES[layer.dtype]
-    _check("moe_forward_host", _lib.moe_forward_host(
+    dev, dt = _device_of(ws), _DTYPES.get(layer.dtype, x_host.dtype)
+    st = _lib.moe_forward_host(
         ctypes.byref(layer), _host_addr(x_host, dt, T * layer.d), T, _host_addr(out_host, dt, T * layer.d),
-        _host_addr(aux_host, _F32, 1), _addr(ws, _U8, 0, dev), ws.numel(), _stream(stream, dev)))
+        _host_addr(aux_host, _F32, 1), _addr(ws, _U8, 0, dev), ws.numel(),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if st != MOE_OK:
+        _check("moe_forward_host", st)
