@@ -46,6 +46,7 @@
 // every other role's path, and takes no tile so early that a slow pair would
 // hold work an idle one could do.
 // Every wait is bounded; a time-out sets MOE_DEVERR_TIMEOUT and unwinds.
+// Times in the comments below are those of short runs, before the power cap.
 #include "mxfp4_gemm.cuh"
 
 namespace moe {
@@ -615,8 +616,8 @@ cudaError_t run_group(const MxRows& a, const MxWeights& b0, const MxWeights& b1,
 // most that can be in use, which is all the host knows) and K is long; single
 // CTAs' 128-row tiles fill better, and with short K a tile's turnaround counts,
 // which the second CTA lengthens. Measured, whole FFN, single against pairs for
-// both products, short runs at 1.7 GHz and up (in a loop under the power cap, at
-// 1.4 to 1.5 GHz, both take a sixth longer): 8 experts, d 4096, F 14336: 32 rows
+// both products, in short runs (back to back, under the power cap, the largest
+// take a sixth longer): 8 experts, d 4096, F 14336: 32 rows
 // an expert 131 / 154 us, 128 rows 166 / 159, 256 rows 229 / 220, 512 rows 377 /
 // 350, 1024 rows 659 / 570; 64 experts, d 4096, F 2048, skewed, 128 rows 182 /
 // 208, 512 rows 469 / 457; d 2048, F 1408: 256 rows 116 / 115, 512 rows 189 /
