@@ -401,7 +401,7 @@ def moe_combine_backward(d_out, y_perm, topk_w, slot_to_row, T, d, k, rows_max, 
     st = _lib.moe_combine_backward(
         _addr(d_out, dt, T * d, dev), _addr(y_perm, dt, row_values, dev), _addr(topk_w, _F32, slots, dev),
         _addr(slot_to_row, _I32, slots, dev), _CODES[dt], T, d, k, rows_max,
-        _addr(d_y_perm, dt, row_values, dev), _addr(d_topk_w, _F32, slots, dev), _addr(ws, _U8, 0, dev),
+        _addr(d_y_perm, dt, row_values, dev), _addr(d_topk_w, _F32, slots, dev), _addr(ws, ws.dtype, 0, dev),
         ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_combine_backward", st)
@@ -413,7 +413,7 @@ def moe_gather_backward(d_x_perm, slot_to_row, dx_in, T, d, k, rows_max, dx, ws,
     st = _lib.moe_gather_backward(
         _addr(d_x_perm, dt, rows_max * d, dev), _addr(slot_to_row, _I32, T * k, dev),
         _addr(dx_in, dt, T * d, dev), _CODES[dt], T, d, k, rows_max, _addr(dx, dt, T * d, dev),
-        _addr(ws, _U8, 0, dev), ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
+        _addr(ws, ws.dtype, 0, dev), ws.numel(), _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_gather_backward", st)
 
@@ -453,7 +453,7 @@ def moe_gather_mxfp4(x, T, d, k, slot_to_row, seg_offsets, E, rows_max, codes, s
     st = _lib.moe_gather_mxfp4(
         _addr(x, dt, T * d, dev), _CODES[dt], T, d, k, _addr(slot_to_row, _I32, T * k, dev),
         _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, _addr(codes, _U8, rows_max * d // 2, dev),
-        _addr(scales, _U8, (rows_max // 128 + E) * (d // 128) * 512, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _addr(scales, _U8, (rows_max // 128 + E) * (d // 128) * 512, dev), _addr(ws, ws.dtype, 0, dev), ws.numel(),
         _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_gather_mxfp4", st)
@@ -465,7 +465,7 @@ def moe_mxfp4_dequantize_rows(codes, scales, seg_offsets, E, rows_max, K, out, w
     st = _lib.moe_mxfp4_dequantize_rows(
         _addr(codes, _U8, rows_max * K // 2, dev), _addr(scales, _U8, (rows_max // 128 + E) * (K // 128) * 512, dev),
         _addr(seg_offsets, _I32, E + 1, dev), E, rows_max, K, _CODES[dt],
-        _addr(out, dt, rows_max * K, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _addr(out, dt, rows_max * K, dev), _addr(ws, ws.dtype, 0, dev), ws.numel(),
         _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_mxfp4_dequantize_rows", st)
@@ -489,7 +489,7 @@ def moe_expert_ffn_mxfp4(x_codes, x_scales, w1, w1_scales, w3, w3_scales, w2, w2
         _addr(w3_scales, _U8, matrix_scales, dev), _addr(w2, _U8, matrix, dev),
         _addr(w2_scales, _U8, matrix_scales, dev), act, rows_max, d, F, E, _addr(seg_offsets, _I32, E + 1, dev),
         _addr(h_codes, _U8, rows_max * F // 2, dev), _addr(h_scales, _U8, groups * (F // 128) * 512, dev),
-        _addr(y_perm, torch.bfloat16, rows_max * d, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _addr(y_perm, torch.bfloat16, rows_max * d, dev), _addr(ws, ws.dtype, 0, dev), ws.numel(),
         _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_expert_ffn_mxfp4", st)
@@ -551,7 +551,7 @@ def moe_forward(layer: MoeLayerC, x, T, out, aux_loss, ws, stream=None, events=N
     dev, dt = _device_of(ws), _DTYPES.get(layer.dtype, x.dtype)
     st = _lib.moe_forward(
         ctypes.byref(layer), _addr(x, dt, T * layer.d, dev), T, _addr(out, dt, T * layer.d, dev),
-        _addr(aux_loss, _F32, 1, dev), _addr(ws, _U8, 0, dev), ws.numel(),
+        _addr(aux_loss, _F32, 1, dev), _addr(ws, ws.dtype, 0, dev), ws.numel(),
         _raw_stream(dev) if stream is None else _stream(stream), ev)
     if st != MOE_OK:
         _check("moe_forward", st)
@@ -568,7 +568,7 @@ def moe_forward_host(layer: MoeLayerC, x_host, T, out_host, aux_host, ws, stream
     dev, dt = _device_of(ws), _DTYPES.get(layer.dtype, x_host.dtype)
     st = _lib.moe_forward_host(
         ctypes.byref(layer), _host_addr(x_host, dt, T * layer.d), T, _host_addr(out_host, dt, T * layer.d),
-        _host_addr(aux_host, _F32, 1), _addr(ws, _U8, 0, dev), ws.numel(),
+        _host_addr(aux_host, _F32, 1), _addr(ws, ws.dtype, 0, dev), ws.numel(),
         _raw_stream(dev) if stream is None else _stream(stream))
     if st != MOE_OK:
         _check("moe_forward_host", st)

@@ -84,7 +84,8 @@ class MoeLayer:
         or (stream given) the one that calls on `stream` use. Calls on two
         streams may run at the same time, so every stream has its own, and
         calls that are captured into a graph have one in the graph's memory,
-        which every replay initialises; `slot` keeps more of them apart."""
+        which every replay initialises (there is nothing to read in it before
+        the first); `slot` keeps more of them apart."""
         if stream is None and (T, host_io, slot) in self._last:
             return self._last[T, host_io, slot]
         return self._workspace(T, host_io, stream, slot)
